@@ -1,0 +1,85 @@
+/*
+ * onetrans_input.h - C ABI of the OneTrans input layer on B200 (sm_100a):
+ * embedding tables and the routed event tokenizer, each with its gradient.
+ * They lead from item ids to the S-tokens that onetrans_stage1_encode,
+ * onetrans_forward and onetrans_forward_backward take, and from the input
+ * gradient that onetrans_forward_backward writes back to the tables:
+ *
+ *   ids -> onetrans_embedding_lookup -> events -> onetrans_route_events,
+ *   onetrans_tokenize_routed -> S-tokens -> the block stack -> dx0
+ *   -> onetrans_tokenize_routed_backward -> event gradients
+ *   -> onetrans_embedding_backward(_sparse) -> table gradients
+ *
+ * The conventions of onetrans.h hold: device pointers owned by the caller and
+ * 16-byte aligned (workspaces and plans 256-byte), the model's mode as element
+ * type unless said otherwise, nothing allocated, calls asynchronous on
+ * `stream`, argument errors found on the host before any launch, a call with
+ * no work returns ONETRANS_OK and launches nothing.  Every call may be
+ * captured into a CUDA graph.  Two calls that may run at the same time need
+ * workspaces (and plans, unless both only read one) of their own; that
+ * includes two graphs that are replayed at the same time.  Sums are float32
+ * and added in a fixed order: equal inputs give equal bits.
+ */
+#ifndef ONETRANS_INPUT_H
+#define ONETRANS_INPUT_H
+
+#include "onetrans.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Which buffer onetrans_input_workspace_size() sizes. */
+typedef enum {
+  ONETRANS_OP_EMBEDDING_BACKWARD = 0, /* n = R ids,    L = width */
+  ONETRANS_OP_ROUTE = 1,              /* the plan: n = R events, L = k */
+  ONETRANS_OP_ROUTED = 2,             /* n = R events, L = k */
+  ONETRANS_OP_ROUTED_BACKWARD = 3     /* n = R events, L = k */
+} onetrans_input_op;
+
+ONETRANS_API onetrans_status onetrans_input_workspace_size(const onetrans_model* m, int32_t op, int64_t n,
+                                                           int32_t L, size_t* bytes);
+
+/* ------------------------------------------------------- embedding tables --
+ * The tables are arguments, not part of the model, and stay the caller's.
+ * ids: int32 (ids_bits 32) or int64 (ids_bits 64).  Id -1 is padding; any
+ * other id outside 0 .. n_rows-1 counts as padding too and sets the device
+ * status word (code 3).  n_rows <= 2^31 - 1, width <= 65536. */
+
+/* out[r] = scale * table[ids[r]] (a zero row for padding), R rows.
+ *   table [n_rows, width] of element type table_mode (ONETRANS_BF16 or
+ *   ONETRANS_FP32); out: rows of the mode's type, out_ld >= width elements
+ *   apart (so that the fields of one feature row can be looked up side by
+ *   side); what lies between two rows is left as it was.  The product is
+ *   taken in float32 and rounded once. */
+ONETRANS_API onetrans_status onetrans_embedding_lookup(const onetrans_model* m, const void* table,
+                                                       int32_t table_mode, int64_t n_rows, int32_t width,
+                                                       const void* ids, int32_t ids_bits, int64_t R, float scale,
+                                                       void* out, int64_t out_ld, void* stream);
+
+/* The gradient of a lookup, dense: dtable[v] = scale * (sum of dout[r] over
+ * the r with ids[r] = v), float32, every row of dtable [n_rows, width]
+ * written (zeros where no id names it).
+ *   dout: rows of element type dout_mode, dout_ld >= width elements apart.
+ * R = 0 still writes the zeros.  R <= 2^26.  Workspace:
+ * ONETRANS_OP_EMBEDDING_BACKWARD. */
+ONETRANS_API onetrans_status onetrans_embedding_backward(const onetrans_model* m, const void* dout,
+                                                         int32_t dout_mode, int64_t dout_ld, const void* ids,
+                                                         int32_t ids_bits, int64_t R, int64_t n_rows,
+                                                         int32_t width, float scale, float* dtable, void* ws,
+                                                         size_t ws_bytes, void* stream);
+
+/* The same gradient as the touched rows only: uniq[i] (the ids' type)
+ * ascending, rows[i] [width] float32 the sum of row uniq[i], i < *n_uniq.
+ * uniq and rows have room for min(R, n_rows) rows; rows at and behind *n_uniq
+ * are left as they were.  n_uniq: int32 on the device (16-byte aligned like
+ * every buffer).  R = 0 writes *n_uniq = 0. */
+ONETRANS_API onetrans_status onetrans_embedding_backward_sparse(
+    const onetrans_model* m, const void* dout, int32_t dout_mode, int64_t dout_ld, const void* ids,
+    int32_t ids_bits, int64_t R, int64_t n_rows, int32_t width, float scale, void* uniq, float* rows,
+    int32_t* n_uniq, void* ws, size_t ws_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* ONETRANS_INPUT_H */

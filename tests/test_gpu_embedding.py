@@ -1,0 +1,285 @@
+"""Embedding lookup with scaling and its gradient by sorted ids, through the C
+ABI against plain float64 implementations.
+
+Tolerances.  A lookup is one float32 product rounded once: float32 output
+within half a step (2^-24 of the value, the product itself; a bf16 or float32
+table entry is exact in float32), bf16 output 2^-8 of the value plus the
+product's own 2^-24.  A gradient entry is a float32 sum of n terms: every
+addition is off by at most 2^-24 of its partial sum, which sum |terms| bounds,
+and a term passes through fewer than n additions, so the error is at most
+n * 2^-24 * sum |terms|, plus one rounding for the scale."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from helpers import build, shape
+
+import unified_transformer_recommender_b200 as ot  # noqa: E402
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+_models = {}
+
+
+def model(mode):
+    if mode not in _models:
+        _models[mode] = build(shape(n_layers=1, d=64, H=1, dff=64, L_NS=1, F=16), 5, mode).model
+    return _models[mode]
+
+
+def make_ids(kind, R, V, seed, dtype=torch.int32):
+    g = np.random.default_rng(seed)
+    if kind == "uniform":
+        ids = g.integers(0, V, R)
+    elif kind == "popular":
+        ids = ((V + 1.0) ** g.random(R) - 1).astype(np.int64).clip(0, V - 1)
+    elif kind == "one":
+        ids = np.full(R, V - 1)
+    elif kind == "padding":
+        ids = np.full(R, -1)
+    else:                                    # every id once, descending
+        ids = np.arange(R)[::-1] % V
+    if kind in ("uniform", "popular"):
+        ids[g.random(R) < 0.1] = -1
+    return torch.from_numpy(ids.copy()).to("cuda", dtype)
+
+
+@pytest.mark.parametrize("mode,table_t,ids_t,R,V,w,pad", [
+    ("bf16", "bf16", torch.int32, 1, 1, 1, 0),
+    ("bf16", "bf16", torch.int32, 1000, 501, 64, 0),
+    ("bf16", "fp32", torch.int64, 777, 333, 50, 14),     # a field inside a wider feature row
+    ("fp32", "bf16", torch.int64, 129, 70, 7, 2),
+    ("fp32", "fp32", torch.int32, 2049, 100, 300, 0),
+    ("bf16", "bf16", torch.int32, 70001, 5003, 16, 0),
+])
+def test_lookup(mode, table_t, ids_t, R, V, w, pad):
+    g = torch.Generator(device="cuda").manual_seed(R)
+    table = torch.randn(V, w, device="cuda", generator=g).to(DT[table_t])
+    ids = make_ids("uniform", R, V, R + 1, ids_t)
+    buf = torch.full((R, w + pad), 7.0, device="cuda", dtype=DT[mode])
+    off = 8 if pad >= 8 else 0                # a column offset that keeps 16-byte alignment
+    out = buf[:, off:off + w]
+    ot.onetrans_embedding_lookup(model(mode), table, ids, out, scale=1.7)
+    torch.cuda.synchronize()
+    assert ot.onetrans_device_status() == 0
+    scale = float(np.float32(1.7))
+    ref = torch.where((ids >= 0)[:, None], table[ids.clamp(min=0).long()].double() * scale, 0.0)
+    err = (out.double() - ref).abs()
+    assert (err <= ref.abs() * (HALF[mode] * (1 + 2.0 ** -8) + 2.0 ** -24)).all()
+    rest = torch.ones(w + pad, dtype=torch.bool)
+    rest[off:off + w] = False
+    assert (buf[:, rest.cuda()] == 7.0).all()     # what lies between two rows is left as it was
+
+
+def test_lookup_flags_ids_out_of_range():
+    table = torch.ones(10, 8, device="cuda", dtype=torch.bfloat16)
+    for bad in (10, -2, 2 ** 31 - 1):
+        ids = torch.tensor([3, bad, -1], device="cuda", dtype=torch.int32)
+        out = torch.full((3, 8), 5.0, device="cuda", dtype=torch.bfloat16)
+        ot.onetrans_embedding_lookup(model("bf16"), table, ids, out)
+        assert ot.onetrans_device_status() == 3
+        assert (out[0] == 1).all() and (out[1:] == 0).all()
+    ids = torch.tensor([2 ** 40 + 1, 9], device="cuda")
+    out = torch.full((2, 8), 5.0, device="cuda", dtype=torch.bfloat16)
+    ot.onetrans_embedding_lookup(model("bf16"), table, ids, out)
+    assert ot.onetrans_device_status() == 3
+    assert (out[0] == 0).all() and (out[1] == 1).all()
+
+
+def test_lookup_offsets_past_32_bits():
+    V, w = 40_000_000, 64                          # 2.56e9 elements
+    table = torch.empty(V, w, device="cuda", dtype=torch.bfloat16)
+    rows = torch.tensor([0, V // 2, V - 1, 33_554_433], device="cuda")
+    for i, r in enumerate(rows.tolist()):
+        table[r] = i + 1
+    out = torch.zeros(4, w, device="cuda", dtype=torch.bfloat16)
+    ot.onetrans_embedding_lookup(model("bf16"), table, rows, out)
+    assert torch.equal(out, torch.arange(1, 5, device="cuda", dtype=torch.bfloat16)[:, None].expand(4, w))
+
+
+def reference(dout, ids, V, scale):
+    """float64 sums [V, w], sums of absolute values, occurrences [V]."""
+    ok = torch.nonzero((ids >= 0) & (ids < V))[:, 0]
+    at = ids[ok].long()
+    x = dout[ok].double()
+    s = torch.zeros(V, dout.shape[1], device="cuda", dtype=torch.float64)
+    m = torch.zeros_like(s)
+    s.index_add_(0, at, x)
+    m.index_add_(0, at, x.abs())
+    n = torch.bincount(at, minlength=V)
+    return s * scale, m * abs(scale), n
+
+
+def check_rows(got, s, m, n):
+    err = (got.double() - s).abs()
+    bound = m * ((n[:, None] + 1) * 2.0 ** -24)
+    assert (err <= bound).all(), float((err - bound).max())
+
+
+GRADS = [
+    # kind, dout type, ids type, R, V, w
+    ("uniform", "bf16", torch.int32, 1, 1, 1),
+    ("uniform", "fp32", torch.int64, 31, 5, 3),
+    ("popular", "bf16", torch.int32, 256, 1000, 64),
+    ("popular", "bf16", torch.int32, 257, 3, 64),          # runs across the warps' and chunks' borders
+    ("one", "fp32", torch.int32, 4096, 2, 40),             # one run through every chunk
+    ("padding", "bf16", torch.int32, 700, 50, 16),         # nothing to add
+    ("each", "bf16", torch.int64, 5000, 5000, 24),         # every id once
+    ("uniform", "bf16", torch.int32, 4097, 7, 300),        # two tiles, several column blocks
+    ("popular", "fp32", torch.int64, 20011, 2_000_000, 50),
+    ("one", "bf16", torch.int64, 30000, 100_000, 128),
+    ("popular", "bf16", torch.int32, 75_392, 1_000_000, 64),
+    ("uniform", "fp32", torch.int32, 270_001, 60_000, 20),  # more tiles than a pass adds up itself
+    ("popular", "bf16", torch.int32, 300_000, 2_147_483_647, 8),   # three passes
+    ("popular", "bf16", torch.int32, 1_100_000, 5_000, 16),        # chunks of more rows
+]
+
+
+@pytest.mark.parametrize("kind,dout_t,ids_t,R,V,w", GRADS)
+def test_gradient_sparse(kind, dout_t, ids_t, R, V, w):
+    g = torch.Generator(device="cuda").manual_seed(R)
+    dout = torch.randn(R, w, device="cuda", generator=g).to(DT[dout_t])
+    ids = make_ids(kind, R, V, R + 2, ids_t)
+    m = model("bf16")
+    room = min(R, V)
+    uniq = torch.full((room,), -7, device="cuda", dtype=ids_t)
+    rows = torch.full((room, w), 7.0, device="cuda")
+    n = torch.full((1,), -1, device="cuda", dtype=torch.int32)
+    ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w)
+    ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, rows, n, ws, scale=0.3)
+    torch.cuda.synchronize()
+    assert ot.onetrans_device_status() == 0
+    ref = torch.unique(ids[ids >= 0])
+    U = int(n.item())
+    assert U == ref.numel()
+    assert torch.equal(uniq[:U], ref)
+    assert (uniq[U:] == -7).all() and (rows[U:] == 7.0).all()     # rows behind the last stay as they were
+    scale = float(np.float32(0.3))
+    pos = torch.where(ids >= 0, torch.searchsorted(ref, ids), torch.full_like(ids, -1))
+    if U:
+        check_rows(rows[:U], *reference(dout, pos, U, scale))
+    again = torch.zeros_like(rows)
+    ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, again, n, ws, scale=0.3)
+    assert torch.equal(again[:U], rows[:U])                       # a fixed order of additions
+
+
+@pytest.mark.parametrize("kind,dout_t,ids_t,R,V,w", [c for c in GRADS if c[4] <= 2_000_000])
+def test_gradient_dense(kind, dout_t, ids_t, R, V, w):
+    g = torch.Generator(device="cuda").manual_seed(R)
+    wide = torch.randn(R, w + 8, device="cuda", generator=g).to(DT[dout_t])
+    dout = wide[:, :w]                                            # rows of a wider gradient
+    ids = make_ids(kind, R, V, R + 3, ids_t)
+    m = model("fp32")
+    dtable = torch.full((V, w), float("nan"), device="cuda")
+    ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w)
+    ot.onetrans_embedding_backward(m, dout, ids, dtable, ws, scale=-2.5)
+    torch.cuda.synchronize()
+    assert ot.onetrans_device_status() == 0
+    s, mag, n = reference(dout, ids, V, -2.5)
+    check_rows(dtable, s, mag, n)
+    assert (dtable[n == 0] == 0).all()
+
+
+def test_gradient_flags_and_skips_ids_out_of_range():
+    ids = torch.tensor([4, 1, 9, -3, 1, -1], device="cuda", dtype=torch.int32)
+    dout = torch.arange(1, 7, device="cuda", dtype=torch.float32)[:, None].expand(6, 4).contiguous()
+    dtable = torch.full((5, 4), float("nan"), device="cuda")
+    m = model("fp32")
+    ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, 6, 4)
+    ot.onetrans_embedding_backward(m, dout, ids, dtable, ws)
+    assert ot.onetrans_device_status() == 3
+    ref = torch.tensor([0.0, 7.0, 0.0, 0.0, 1.0], device="cuda")[:, None].expand(5, 4)
+    assert torch.equal(dtable, ref)
+
+
+def test_gradient_keeps_infinities_and_nan_in_their_rows():
+    R, V, w = 3000, 50, 64
+    ids = make_ids("uniform", R, V, 9)
+    dout = torch.randn(R, w, device="cuda")
+    hit = int(torch.nonzero(ids == 3)[0])
+    nan = int(torch.nonzero(ids == 7)[0])
+    dout[hit, 5], dout[nan, 6] = float("inf"), float("nan")
+    dout[ids == -1] = float("nan")                                # padding rows are not read into any sum
+    m = model("bf16")
+    dtable = torch.zeros(V, w, device="cuda")
+    ot.onetrans_embedding_backward(m, dout, ids, dtable, m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w))
+    bad = ~torch.isfinite(dtable)
+    assert bad[3, 5] and bad[7, 6] and int(bad.sum()) == 2
+
+
+def test_no_ids():
+    m = model("bf16")
+    none = torch.empty(0, device="cuda", dtype=torch.int32)
+    ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, 0, 8)
+    n = torch.full((1,), 5, device="cuda", dtype=torch.int32)
+    e = torch.empty(0, 8, device="cuda")
+    ot.onetrans_embedding_backward_sparse(m, e, none, 10, none, e, n, ws)
+    assert int(n.item()) == 0
+    dtable = torch.full((10, 8), 3.0, device="cuda")
+    ot.onetrans_embedding_backward(m, e, none, dtable, ws)
+    assert (dtable == 0).all()
+    ot.onetrans_embedding_lookup(m, torch.zeros(3, 8, device="cuda"), none, torch.empty(0, 8, device="cuda", dtype=torch.bfloat16))
+
+
+def test_captured_and_on_another_stream():
+    """A lookup and both gradients captured on a side stream, replayed on new inputs in the same buffers."""
+    m = model("fp32")
+    R, V, w = 9000, 4000, 48
+    table = torch.randn(V, w, device="cuda")
+    ids = make_ids("popular", R, V, 21)
+    out, dtable = torch.empty(R, w, device="cuda"), torch.empty(V, w, device="cuda")
+    uniq, rows = torch.empty(V, device="cuda", dtype=torch.int32), torch.empty(V, w, device="cuda")
+    n = torch.empty(1, device="cuda", dtype=torch.int32)
+    ws = [m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w) for _ in range(2)]
+
+    def step():
+        ot.onetrans_embedding_lookup(m, table, ids, out, scale=2.0)
+        ot.onetrans_embedding_backward(m, out, ids, dtable, ws[0])
+        ot.onetrans_embedding_backward_sparse(m, out, ids, V, uniq, rows, n, ws[1])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (22, 23):
+        ids.copy_(make_ids("popular", R, V, seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        s, mag, cnt = reference(out, ids, V, 1.0)
+        check_rows(dtable, s, mag, cnt)
+        U = int(n.item())
+        assert torch.equal(uniq[:U].long(), torch.nonzero(cnt)[:, 0])
+        assert torch.equal(rows[:U], dtable[cnt > 0])
+    assert ot.onetrans_device_status() == 0
+
+
+def test_finite_differences():
+    """The gradient of f(table) = sum(c * lookup(table)) against central differences of the lookup itself."""
+    m = model("fp32")
+    R, V, w = 200, 37, 9
+    g = torch.Generator(device="cuda").manual_seed(3)
+    table = torch.randn(V, w, device="cuda", generator=g)
+    c = torch.randn(R, w, device="cuda", generator=g)
+    ids = make_ids("uniform", R, V, 31)
+    dtable = torch.empty(V, w, device="cuda")
+    ot.onetrans_embedding_backward(m, c, ids, dtable, m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w), scale=1.5)
+
+    def f(t):
+        out = torch.empty(R, w, device="cuda")
+        ot.onetrans_embedding_lookup(m, t, ids, out, scale=1.5)
+        return float((out.double() * c.double()).sum())
+
+    for seed in range(4):
+        v = torch.randn(V, w, device="cuda", generator=g)
+        # the lookup is linear: a unit step has no truncation error, only the lookups' own
+        # roundings (2^-24 of about 2 * 1.5 * (|t| + |v|) per entry, and of the sum table + v)
+        diff = (f(table + v) - f(table - v)) / 2
+        ref = float((dtable.double() * v.double()).sum())
+        size = float((c.double().abs() * 1.5 * (table.abs() + v.abs())[ids.clamp(min=0).long()].double()).sum())
+        assert abs(diff - ref) <= size * 8 * 2.0 ** -24

@@ -1,0 +1,82 @@
+"""Host side of the input layer's C ABI (include/onetrans_input.h), without a
+GPU: exports, workspace sizes, and argument errors found before any launch.
+Device pointers are fake aligned addresses; nothing here reaches a kernel."""
+import ctypes
+import os
+import re
+
+import unified_transformer_recommender_b200 as ot
+from test_host_abi import FAKE, FakeModel
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "onetrans_input.h")
+BIG = 1 << 40
+
+
+def size_of(fm, op, n, L):
+    out = ot.SZ(0)
+    return ot.lib.onetrans_input_workspace_size(fm.h, op, n, L, ctypes.byref(out)), out.value
+
+
+def test_exports():
+    names = set(re.findall(r"ONETRANS_API\s+[\w\s\*]+?\b(onetrans_\w+)\s*\(", open(HEADER).read()))
+    assert names == set(ot.INPUT_SYMBOLS)
+    for n in names:
+        assert hasattr(ot.lib, n), n
+
+
+def test_embedding_workspace():
+    fm = FakeModel()
+    st, a = size_of(fm, ot.OP_EMBEDDING_BACKWARD, 1000, 64)
+    st2, b = size_of(fm, ot.OP_EMBEDDING_BACKWARD, 100_000, 64)
+    assert st == st2 == ot.OK and 16 * 1000 <= a < b and b >= 16 * 100_000
+    assert size_of(fm, ot.OP_EMBEDDING_BACKWARD, -1, 64)[0] == ot.ERR_SHAPE
+    assert size_of(fm, ot.OP_EMBEDDING_BACKWARD, 2 ** 26 + 1, 64)[0] == ot.ERR_SHAPE
+    assert size_of(fm, ot.OP_EMBEDDING_BACKWARD, 10, 0)[0] == ot.ERR_SHAPE
+    assert size_of(fm, 99, 10, 1)[0] == ot.ERR_INVALID_ARG
+    assert ot.lib.onetrans_input_workspace_size(None, 0, 1, 1, ctypes.byref(ot.SZ(0))) == ot.ERR_INVALID_ARG
+
+
+def test_lookup_argument_errors():
+    fm = FakeModel()
+    base = dict(m=fm.h, table=FAKE, tm=ot.BF16, V=100, w=64, ids=FAKE, bits=32, R=8, out=FAKE, ld=64)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return ot.lib.onetrans_embedding_lookup(a["m"], a["table"], a["tm"], a["V"], a["w"], a["ids"], a["bits"], a["R"],
+                                                1.0, a["out"], a["ld"], None)
+
+    assert call(R=0, table=None, ids=None, out=None) == ot.OK
+    for kw in (dict(m=None), dict(tm=2), dict(bits=16), dict(table=None), dict(ids=None), dict(out=None),
+               dict(table=FAKE + 8), dict(ids=FAKE + 4), dict(out=FAKE + 2)):
+        assert call(**kw) == ot.ERR_INVALID_ARG, kw
+    for kw in (dict(V=0), dict(V=2 ** 31), dict(w=0), dict(w=65537, ld=70000), dict(R=-1), dict(R=2 ** 31), dict(ld=63)):
+        assert call(**kw) == ot.ERR_SHAPE, kw
+
+
+def test_gradient_argument_errors():
+    fm = FakeModel()
+    base = dict(m=fm.h, dout=FAKE, dm=ot.BF16, ld=64, ids=FAKE, bits=32, R=8, V=100, w=64, out=FAKE, uniq=FAKE, n=FAKE,
+                ws=FAKE, nb=BIG)
+
+    def dense(**kw):
+        a = dict(base, **kw)
+        return ot.lib.onetrans_embedding_backward(a["m"], a["dout"], a["dm"], a["ld"], a["ids"], a["bits"], a["R"],
+                                                  a["V"], a["w"], 1.0, a["out"], a["ws"], a["nb"], None)
+
+    def sparse(**kw):
+        a = dict(base, **kw)
+        return ot.lib.onetrans_embedding_backward_sparse(a["m"], a["dout"], a["dm"], a["ld"], a["ids"], a["bits"], a["R"],
+                                                         a["V"], a["w"], 1.0, a["uniq"], a["out"], a["n"], a["ws"],
+                                                         a["nb"], None)
+
+    for f in (dense, sparse):
+        for kw in (dict(m=None), dict(dm=3), dict(bits=8), dict(dout=None), dict(ids=None), dict(ws=None), dict(out=None),
+                   dict(dout=FAKE + 2), dict(ids=FAKE + 4), dict(out=FAKE + 4), dict(ws=FAKE + 16)):
+            assert f(**kw) == ot.ERR_INVALID_ARG, kw
+        for kw in (dict(V=0), dict(V=2 ** 31), dict(w=0), dict(R=-1), dict(R=2 ** 26 + 1), dict(ld=63)):
+            assert f(**kw) == ot.ERR_SHAPE, kw
+        need = size_of(fm, ot.OP_EMBEDDING_BACKWARD, 8, 64)[1]
+        assert f(nb=need - 1) == ot.ERR_CAPACITY
+    for kw in (dict(uniq=None), dict(uniq=FAKE + 8), dict(n=None), dict(n=FAKE + 4)):
+        assert sparse(**kw) == ot.ERR_INVALID_ARG, kw
+    assert dense(R=0, out=None) == ot.ERR_INVALID_ARG      # the zeros still have to go somewhere

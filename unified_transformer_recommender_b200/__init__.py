@@ -1,4 +1,5 @@
-"""Python binding of the OneTrans B200 library (ctypes over include/onetrans.h).
+"""Python binding of the OneTrans B200 library (ctypes over include/onetrans.h
+and include/onetrans_input.h).
 
 Argument marshalling only: every step of the path runs in the CUDA library
 `libonetrans.so` built in this directory.  PyTorch supplies device memory and
@@ -22,6 +23,8 @@ LIB_PATH = os.path.join(_HERE, "libonetrans.so")
 OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_CUDA, ERR_DEVICE_CHECK = 0, -1, -2, -3, -4, -5, -6
 BF16, FP32 = 0, 1
 OP_FORWARD, OP_STAGE1, OP_STAGE2, OP_APPEND, OP_AUTOSPLIT, OP_GROUPWISE, OP_TRAIN = 0, 1, 2, 3, 4, 5, 6
+# of the input layer (Model.input_workspace)
+OP_EMBEDDING_BACKWARD, OP_ROUTE, OP_ROUTED, OP_ROUTED_BACKWARD = 0, 1, 2, 3
 
 SYMBOLS = (
     "onetrans_model_create", "onetrans_model_destroy", "onetrans_workspace_size",
@@ -34,6 +37,11 @@ SYMBOLS = (
     "onetrans_profile_enable", "onetrans_profile_kinds", "onetrans_profile_read",
     "onetrans_tokenize_autosplit_static", "onetrans_tokenize_events", "onetrans_merge_intent_order",
     "onetrans_tokenize_groupwise", "onetrans_selftest_bounded_wait", "onetrans_forward_backward",
+)
+# declared in include/onetrans_input.h
+INPUT_SYMBOLS = (
+    "onetrans_input_workspace_size", "onetrans_embedding_lookup", "onetrans_embedding_backward",
+    "onetrans_embedding_backward_sparse",
 )
 
 
@@ -113,6 +121,11 @@ _sig("onetrans_merge_intent_order", I32, P, P, PI64, PI32, I32, P, P, P)
 _sig("onetrans_tokenize_groupwise", I32, P, P, I64, I32, I32, I32, P, P, P, P, P, P, SZ, P)
 _sig("onetrans_forward", I32, P, P, I32, I32, P, P, SZ, P)
 _sig("onetrans_forward_backward", I32, P, P, I32, I32, P, P, P, P, P, SZ, P)
+_sig("onetrans_input_workspace_size", I32, P, I32, I64, I32, ctypes.POINTER(SZ))
+_sig("onetrans_embedding_lookup", I32, P, P, I32, I64, I32, P, I32, I64, ctypes.c_float, P, I64, P)
+_sig("onetrans_embedding_backward", I32, P, P, I32, I64, P, I32, I64, I64, I32, ctypes.c_float, P, P, SZ, P)
+_sig("onetrans_embedding_backward_sparse", I32, P, P, I32, I64, P, I32, I64, I64, I32, ctypes.c_float, P, P, P, P, SZ,
+     P)
 _sig("onetrans_set_kernel_policy", I32, I32)
 _sig("onetrans_device_status", I32, P, PI32)
 _sig("onetrans_selftest_bounded_wait", I32, I32, P)
@@ -239,6 +252,15 @@ class Model:
 
     def workspace(self, op: int, n: int, L: int = 0, device="cuda") -> torch.Tensor:
         return torch.empty(max(self.workspace_size(op, n, L), 256), dtype=torch.uint8, device=device)
+
+    def input_workspace_size(self, op: int, n: int, L: int) -> int:
+        out = SZ(0)
+        _check("onetrans_input_workspace_size",
+               lib.onetrans_input_workspace_size(self.handle, op, n, L, ctypes.byref(out)))
+        return out.value
+
+    def input_workspace(self, op: int, n: int, L: int, device="cuda") -> torch.Tensor:
+        return torch.empty(max(self.input_workspace_size(op, n, L), 256), dtype=torch.uint8, device=device)
 
     def schedule(self, L_S: int):
         out = (I32 * self.n_layers)()
@@ -420,3 +442,86 @@ def onetrans_forward_backward(model: Model, x0: torch.Tensor, dy: torch.Tensor, 
     _check("onetrans_forward_backward", lib.onetrans_forward_backward(
         model.handle, _ptr(x0), B, L0 - model.L_NS, _ptr(dy), _ptr(out), _ptr(dx0), ctypes.byref(g), _ptr(ws),
         ws.numel(), _stream(stream)))
+
+
+# -------------------------------------------------------------- input layer
+
+_MODE_OF = {torch.bfloat16: BF16, torch.float32: FP32}
+_ID_BITS = {torch.int32: 32, torch.int64: 64}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_one_device(*tensors: Optional[torch.Tensor]) -> None:
+    """Every tensor on the current CUDA device, where the call's kernels run."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"tensors must be on the current CUDA device ({dev}), got one on {t.device}")
+
+
+def _rows(t: torch.Tensor, what: str):
+    """(leading dimension, width) of a 2-D tensor whose rows are contiguous."""
+    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), f"{what} must be 2-D with contiguous rows")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    _need(ld >= t.shape[1], f"{what}: rows overlap")
+    return ld, t.shape[1]
+
+
+def onetrans_embedding_lookup(model: Model, table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor,
+                              scale: float = 1.0, stream=None) -> None:
+    """out[r] = scale * table[ids[r]]; id -1 gives a zero row.  table [V, w] bf16 or float32; ids [R] int32 or
+    int64; out [R, w] of the model dtype, rows contiguous, any row stride."""
+    _on_one_device(table, ids, out)
+    ld, w = _rows(out, "out")
+    _need(table.dim() == 2 and table.is_contiguous() and table.dtype in _MODE_OF,
+          "table must be a contiguous [V, w] tensor of bfloat16 or float32")
+    _need(ids.dim() == 1 and ids.is_contiguous() and ids.dtype in _ID_BITS,
+          "ids must be a contiguous [R] tensor of int32 or int64")
+    _need(out.dtype == model.dtype and out.shape[0] == ids.shape[0] and w == table.shape[1],
+          "out must be [R, w] of the model dtype")
+    _check("onetrans_embedding_lookup", lib.onetrans_embedding_lookup(
+        model.handle, _ptr(table), _MODE_OF[table.dtype], table.shape[0], w, _ptr(ids), _ID_BITS[ids.dtype],
+        ids.shape[0], scale, _ptr(out), ld, _stream(stream)))
+
+
+def _grad_args(dout: torch.Tensor, ids: torch.Tensor):
+    ld, w = _rows(dout, "dout")
+    _need(dout.dtype in _MODE_OF, "dout must be bfloat16 or float32")
+    _need(ids.dim() == 1 and ids.is_contiguous() and ids.dtype in _ID_BITS and ids.shape[0] == dout.shape[0],
+          "ids must be a contiguous [R] tensor of int32 or int64, one id per row of dout")
+    return ld, w
+
+
+def onetrans_embedding_backward(model: Model, dout: torch.Tensor, ids: torch.Tensor, dtable: torch.Tensor,
+                                ws: torch.Tensor, scale: float = 1.0, stream=None) -> None:
+    """dtable[v] = scale * sum of dout[r] over ids[r] = v, every row of dtable [V, w] float32 written.  dout
+    [R, w] bf16 or float32, rows contiguous, any row stride."""
+    _on_one_device(dout, ids, dtable, ws)
+    ld, w = _grad_args(dout, ids)
+    _need(dtable.dim() == 2 and dtable.is_contiguous() and dtable.dtype == torch.float32 and dtable.shape[1] == w,
+          "dtable must be a contiguous [V, w] float32 tensor")
+    _check("onetrans_embedding_backward", lib.onetrans_embedding_backward(
+        model.handle, _ptr(dout), _MODE_OF[dout.dtype], ld, _ptr(ids), _ID_BITS[ids.dtype], ids.shape[0],
+        dtable.shape[0], w, scale, _ptr(dtable), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def onetrans_embedding_backward_sparse(model: Model, dout: torch.Tensor, ids: torch.Tensor, n_rows: int,
+                                       uniq: torch.Tensor, rows: torch.Tensor, n_uniq: torch.Tensor,
+                                       ws: torch.Tensor, scale: float = 1.0, stream=None) -> None:
+    """The touched rows of the same gradient: uniq (the ids' dtype) ascending, rows [.., w] float32, n_uniq [1]
+    int32 on the device.  uniq and rows hold min(R, n_rows) rows at least; those behind n_uniq stay as they were."""
+    _on_one_device(dout, ids, uniq, rows, n_uniq, ws)
+    ld, w = _grad_args(dout, ids)
+    room = min(ids.shape[0], n_rows)
+    _need(uniq.dim() == 1 and uniq.is_contiguous() and uniq.dtype == ids.dtype and uniq.shape[0] >= room,
+          "uniq must be a contiguous tensor of the ids' dtype with room for min(R, n_rows) ids")
+    _need(rows.dim() == 2 and rows.is_contiguous() and rows.dtype == torch.float32 and rows.shape[1] == w
+          and rows.shape[0] >= room, "rows must be a contiguous float32 tensor with room for min(R, n_rows) rows")
+    _need(n_uniq.numel() == 1 and n_uniq.dtype == torch.int32, "n_uniq must be one int32")
+    _check("onetrans_embedding_backward_sparse", lib.onetrans_embedding_backward_sparse(
+        model.handle, _ptr(dout), _MODE_OF[dout.dtype], ld, _ptr(ids), _ID_BITS[ids.dtype], ids.shape[0], n_rows, w,
+        scale, _ptr(uniq), _ptr(rows), _ptr(n_uniq), _ptr(ws), ws.numel(), _stream(stream)))

@@ -34,7 +34,7 @@ def nvcc() -> str:
 def sources():
     d = os.path.join(HERE, "csrc")
     return [os.path.join(d, f) for f in sorted(os.listdir(d))] + [
-        os.path.join(ROOT, "include", "onetrans.h")]
+        os.path.join(ROOT, "include", f) for f in ("onetrans.h", "onetrans_input.h")]
 
 
 def up_to_date() -> bool:

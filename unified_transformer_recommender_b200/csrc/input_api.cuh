@@ -1,0 +1,266 @@
+// Host side of the input layer's C ABI (onetrans_input.h): checks, workspace
+// carving and launches of the embedding and routed-tokenizer kernels.
+// Included by onetrans.cu after the model, workspace and profiling helpers.
+#pragma once
+
+// Raises a kernel's dynamic shared memory limit on the current device (the
+// attribute is per device and cheap to set again).
+template <typename K>
+static bool allow_smem(K kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ||
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+static const long long kMaxTableRows = 0x7fffffff, kMaxGradIds = 1LL << 26;
+static const int kMaxWidth = 65536;
+
+static bool mode_ok(int32_t mode) { return mode == ONETRANS_BF16 || mode == ONETRANS_FP32; }
+
+// ----------------------------------------------------------------- lookup --
+template <typename Tt, typename To, typename Id>
+static onetrans_status lookup_impl(const void* table, long long n_rows, int width, const void* ids, long long R,
+                                   float scale, void* out, long long out_ld, cudaStream_t st) {
+  // 16 bytes of the wider type's row per access where the rows keep that alignment
+  int ve = sizeof(Tt) == 4 && sizeof(To) == 4 ? 4 : 8;
+  while (width % ve || out_ld % ve) ve >>= 1;
+  const int cpr = width / ve;
+  // about a thousand groups of columns a CTA, fewer when that leaves SMs idle
+  const long long per = std::min<long long>(kLookThreads * kLookUnroll,
+                                            std::max<long long>(kLookThreads, R * cpr / device_sm_count()));
+  const int rows = (int)std::max<long long>(1, per / cpr);
+  const dim3 grid((unsigned)cdiv(R, rows));
+  ProfScope prof(PK_EMBEDDING, 0.0, (double)R * (sizeof(Id) + width * (double)(sizeof(Tt) + sizeof(To))), st);
+  auto go = [&](auto kernel) {
+    launch_dependent(kernel, grid, dim3(kLookThreads), 0, st, (const Tt*)table, (uint32_t)n_rows, width,
+                     (const Id*)ids, R, rows, scale, (To*)out, out_ld);
+  };
+  switch (ve) {
+    case 8: go(emb_lookup_kernel<Tt, To, Id, 8>); break;
+    case 4: go(emb_lookup_kernel<Tt, To, Id, 4>); break;
+    case 2: go(emb_lookup_kernel<Tt, To, Id, 2>); break;
+    default: go(emb_lookup_kernel<Tt, To, Id, 1>); break;
+  }
+  return last_launch();
+}
+
+// ---------------------------------------------------------------- gradient --
+struct EmbGrad {
+  const void* dout;
+  int dout_mode;
+  long long dout_ld;
+  const void* ids;
+  int ids_bits;
+  long long R, n_rows;
+  int width;
+  float scale;
+  float* out;       // dense: the table gradient; sparse: the touched rows
+  void* uniq;       // null: dense
+  int32_t* n_uniq;
+};
+
+static int key_bits(long long n_rows) {
+  int b = 1;
+  while ((n_rows >> b) != 0) ++b;
+  return b;
+}
+
+// Tiles whose counts every CTA of a pass adds up itself; with more, a scan
+// kernel turns them into prefixes first (each CTA reads tiles x digits counts).
+static const int kSortDirectTiles = 64;
+
+template <typename T, typename Id, bool DENSE>
+static onetrans_status emb_reduce_launch(const EmbGrad& g, ReduceArgs a, cudaStream_t st) {
+  int cpl = 1;
+  while (cpl < 8 && 32 * cpl < g.width) cpl *= 2;
+  while (g.width % cpl || g.dout_ld % cpl) cpl >>= 1;
+  const unsigned fill = DENSE ? (unsigned)cdiv(g.n_rows, 256) : 0u;
+  const dim3 grid((unsigned)a.chunks + fill, (unsigned)cdiv(g.width, 32 * cpl));
+  const dim3 jgrid((unsigned)a.chunks, grid.y);
+  auto go = [&](auto reduce, auto join) {
+    launch_dependent(reduce, grid, dim3(32 * kRedWarps), 0, st, (const T*)g.dout, a);
+    if (a.chunks > 1) launch_dependent(join, jgrid, dim3(1024), 0, st, a);
+  };
+  switch (cpl) {
+    case 8: go(emb_reduce_kernel<T, Id, 8, DENSE>, emb_join_kernel<8>); break;
+    case 4: go(emb_reduce_kernel<T, Id, 4, DENSE>, emb_join_kernel<4>); break;
+    case 2: go(emb_reduce_kernel<T, Id, 2, DENSE>, emb_join_kernel<2>); break;
+    default: go(emb_reduce_kernel<T, Id, 1, DENSE>, emb_join_kernel<1>); break;
+  }
+  return last_launch();
+}
+
+template <typename Id>
+static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes, cudaStream_t st, size_t* need) {
+  const long long R = g.R;
+  const int tiles = (int)cdiv(R, kSortTile);
+  // chunks of sorted positions, 4096 chunks at most up to R = 2^20
+  const int chunk = 32 * kRedWarps * (int)cdiv(std::max<long long>(R, 1), 1 << 20);
+  const int chunks = (int)cdiv(R, chunk);
+  Carve cv(ws, ws_bytes);
+  uint32_t* keys[2];
+  uint32_t* vals[2];
+  for (int i = 0; i < 2; ++i) {
+    keys[i] = (uint32_t*)cv.take(R * 4);
+    vals[i] = (uint32_t*)cv.take(R * 4);
+  }
+  const int max_passes = (31 + kSortMaxBits - 1) / kSortMaxBits;
+  int* hist = (int*)cv.take(((size_t)tiles * max_passes + 1) * (sizeof(int) << kSortMaxBits));
+  int* heads = (int*)cv.take((size_t)chunks * 4);
+  float* first = (float*)cv.take((size_t)chunks * g.width * 4);
+  float* tail = (float*)cv.take((size_t)chunks * g.width * 4);
+  int* state = (int*)cv.take((size_t)chunks * 4);
+  long long* tail_row = (long long*)cv.take((size_t)chunks * 8);
+  if (need) {
+    *need = cv.used;
+    return ONETRANS_OK;
+  }
+  if (cv.overflow) return ONETRANS_ERR_CAPACITY;
+
+  const bool dense = !g.uniq;
+  const uint32_t n_rows = (uint32_t)g.n_rows;
+  const int bits = key_bits(g.n_rows);
+  const int passes = (int)cdiv(bits, kSortMaxBits), per = (int)cdiv(bits, passes), bins = 1 << per;
+  const double row_bytes = (double)R * g.width * (g.dout_mode == ONETRANS_BF16 ? 2 : 4);
+  ProfScope prof(PK_EMBEDDING_GRAD, (double)R * g.width,
+                 row_bytes + (double)R * sizeof(Id) +
+                     (double)(dense ? g.n_rows : std::min(R, g.n_rows)) * g.width * 4, st);
+  int at = 0;   // the sorted pairs are in keys[at], vals[at]
+  if (R > 0 && tiles == 1) {
+    const size_t smem = (size_t)kSortWarps * bins * 2 + std::max(bins, 32) * 4 + 2 * kSortTile * 4;
+    if (!allow_smem(sort_small_kernel<Id>, smem)) return ONETRANS_ERR_CUDA;
+    launch_dependent(sort_small_kernel<Id>, dim3(1), dim3(kSortThreads), smem, st, (const Id*)g.ids, n_rows, (int)R,
+                     passes, per, keys[0], vals[0], dense ? (int*)nullptr : heads, chunk);
+  } else if (R > 0) {
+    const long long per_pass = (long long)tiles * bins;
+    SortArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.n_rows = n_rows;
+    a.R = R;
+    a.tiles = tiles;
+    a.bits = per;
+    a.tot = hist + per_pass * passes;
+    a.hist = hist;
+    a.hist_next = hist + per_pass;
+    a.scanned = tiles > kSortDirectTiles;
+    launch_dependent(sort_hist_kernel<Id>, dim3(tiles), dim3(kSortThreads), 0, st, (const Id*)g.ids, a,
+                     per_pass * (passes - 1));
+    const size_t smem = (size_t)kSortWarps * bins * 2 + (size_t)bins * 4;
+    if (!allow_smem(sort_pass_kernel<Id, true>, smem) || !allow_smem(sort_pass_kernel<Id, false>, smem))
+      return ONETRANS_ERR_CUDA;
+    for (int p = 0; p < passes; ++p) {
+      a.shift = p * per;
+      a.hist = hist + per_pass * p;
+      a.hist_next = p + 1 < passes ? a.hist + per_pass : nullptr;
+      if (a.scanned) launch_dependent(sort_scan_kernel, dim3((unsigned)cdiv(bins, 32)), dim3(kSortThreads), 0, st, a);
+      const uint32_t *ki = keys[at], *vi = vals[at];
+      if (p > 0) at ^= 1;
+      if (p == 0)
+        launch_dependent(sort_pass_kernel<Id, true>, dim3(tiles), dim3(kSortThreads), smem, st, (const Id*)g.ids,
+                         (const uint32_t*)nullptr, (const uint32_t*)nullptr, keys[at], vals[at], a, per, a.shift + per);
+      else
+        launch_dependent(sort_pass_kernel<Id, false>, dim3(tiles), dim3(kSortThreads), smem, st, (const Id*)nullptr, ki,
+                         vi, keys[at], vals[at], a, per, a.shift + per);
+    }
+    if (!dense)
+      launch_dependent(emb_heads_kernel, dim3(chunks), dim3(256), 0, st, (const uint32_t*)keys[at], R, n_rows, chunk,
+                       heads);
+  }
+  OT_TRY(last_launch());
+  ReduceArgs r;
+  std::memset(&r, 0, sizeof(r));
+  r.keys = keys[at]; r.vals = vals[at];
+  r.n_rows = n_rows;
+  r.R = R; r.dout_ld = g.dout_ld;
+  r.width = g.width; r.chunk = chunk; r.chunks = chunks;
+  r.scale = g.scale;
+  r.out = g.out; r.uniq = g.uniq; r.n_uniq = g.n_uniq;
+  r.heads = heads; r.first = first; r.tail = tail; r.state = state; r.tail_row = tail_row;
+  if (g.dout_mode == ONETRANS_BF16)
+    return dense ? emb_reduce_launch<__nv_bfloat16, int32_t, true>(g, r, st)
+                 : emb_reduce_launch<__nv_bfloat16, Id, false>(g, r, st);
+  return dense ? emb_reduce_launch<float, int32_t, true>(g, r, st) : emb_reduce_launch<float, Id, false>(g, r, st);
+}
+
+static onetrans_status emb_grad_check(const onetrans_model* m, const EmbGrad& g) {
+  if (!m || !mode_ok(g.dout_mode) || (g.ids_bits != 32 && g.ids_bits != 64)) return ONETRANS_ERR_INVALID_ARG;
+  if (g.R < 0 || g.R > kMaxGradIds || g.n_rows < 1 || g.n_rows > kMaxTableRows || g.width < 1 ||
+      g.width > kMaxWidth || g.dout_ld < g.width)
+    return ONETRANS_ERR_SHAPE;
+  return ONETRANS_OK;
+}
+
+static onetrans_status emb_grad_run(const EmbGrad& g, void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (g.R > 0 && (!g.dout || !g.ids || !ws || !aligned(g.dout, 16) || !aligned(g.ids, 16) || !aligned(ws, 256)))
+    return ONETRANS_ERR_INVALID_ARG;
+  return g.ids_bits == 32 ? emb_grad_impl<int32_t>(g, ws, ws_bytes, st, nullptr)
+                          : emb_grad_impl<int64_t>(g, ws, ws_bytes, st, nullptr);
+}
+
+// ============================================================== C ABI ====
+extern "C" {
+
+onetrans_status onetrans_input_workspace_size(const onetrans_model* m, int32_t op, int64_t n, int32_t L,
+                                              size_t* bytes) {
+  if (!m || !bytes) return ONETRANS_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (n < 0 || L < 1) return ONETRANS_ERR_SHAPE;
+  switch (op) {
+    case ONETRANS_OP_EMBEDDING_BACKWARD: {
+      if (n > kMaxGradIds || L > kMaxWidth) return ONETRANS_ERR_SHAPE;
+      EmbGrad g;
+      std::memset(&g, 0, sizeof(g));
+      g.R = n;
+      g.width = L;
+      return emb_grad_impl<int32_t>(g, nullptr, 0, nullptr, bytes);
+    }
+    default:
+      return ONETRANS_ERR_INVALID_ARG;
+  }
+}
+
+onetrans_status onetrans_embedding_lookup(const onetrans_model* m, const void* table, int32_t table_mode,
+                                          int64_t n_rows, int32_t width, const void* ids, int32_t ids_bits, int64_t R,
+                                          float scale, void* out, int64_t out_ld, void* stream) {
+  if (!m || !mode_ok(table_mode) || (ids_bits != 32 && ids_bits != 64)) return ONETRANS_ERR_INVALID_ARG;
+  if (R < 0 || R > kMaxTableRows || n_rows < 1 || n_rows > kMaxTableRows || width < 1 || width > kMaxWidth ||
+      out_ld < width)
+    return ONETRANS_ERR_SHAPE;
+  if (R == 0) return ONETRANS_OK;
+  if (!table || !ids || !out || !aligned(table, 16) || !aligned(ids, 16) || !aligned(out, 16))
+    return ONETRANS_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool tb = table_mode == ONETRANS_BF16, w = ids_bits == 64;
+  auto go = [&](auto t, auto o) {
+    using Tt = decltype(t);
+    using To = decltype(o);
+    return w ? lookup_impl<Tt, To, int64_t>(table, n_rows, width, ids, R, scale, out, out_ld, st)
+             : lookup_impl<Tt, To, int32_t>(table, n_rows, width, ids, R, scale, out, out_ld, st);
+  };
+  if (tb) return m->bf16 ? go(__nv_bfloat16(), __nv_bfloat16()) : go(__nv_bfloat16(), float());
+  return m->bf16 ? go(float(), __nv_bfloat16()) : go(float(), float());
+}
+
+onetrans_status onetrans_embedding_backward(const onetrans_model* m, const void* dout, int32_t dout_mode,
+                                            int64_t dout_ld, const void* ids, int32_t ids_bits, int64_t R,
+                                            int64_t n_rows, int32_t width, float scale, float* dtable, void* ws,
+                                            size_t ws_bytes, void* stream) {
+  const EmbGrad g{dout, dout_mode, dout_ld, ids, ids_bits, R, n_rows, width, scale, dtable, nullptr, nullptr};
+  OT_TRY(emb_grad_check(m, g));
+  if (!dtable || !aligned(dtable, 16)) return ONETRANS_ERR_INVALID_ARG;
+  return emb_grad_run(g, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+onetrans_status onetrans_embedding_backward_sparse(const onetrans_model* m, const void* dout, int32_t dout_mode,
+                                                   int64_t dout_ld, const void* ids, int32_t ids_bits, int64_t R,
+                                                   int64_t n_rows, int32_t width, float scale, void* uniq,
+                                                   float* rows, int32_t* n_uniq, void* ws, size_t ws_bytes,
+                                                   void* stream) {
+  const EmbGrad g{dout, dout_mode, dout_ld, ids, ids_bits, R, n_rows, width, scale, rows, uniq, n_uniq};
+  OT_TRY(emb_grad_check(m, g));
+  if (!n_uniq || !aligned(n_uniq, 16)) return ONETRANS_ERR_INVALID_ARG;
+  if (R == 0) return cuda_ok(cudaMemsetAsync(n_uniq, 0, sizeof(int32_t), (cudaStream_t)stream));
+  if (!uniq || !rows || !aligned(uniq, 16) || !aligned(rows, 16)) return ONETRANS_ERR_INVALID_ARG;
+  return emb_grad_run(g, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -2,6 +2,7 @@
 // paged-cache bookkeeping and the launch sequence of every entry point.
 // All kernels live in this one translation unit (see the included headers).
 #include "onetrans.h"
+#include "onetrans_input.h"
 
 #include <algorithm>
 #include <cmath>
@@ -21,6 +22,7 @@
 #include "backward.cuh"
 #include "attn_train.cuh"
 #include "gemm_wgrad.cuh"
+#include "embedding.cuh"
 
 using namespace ot;
 
@@ -55,12 +57,14 @@ static int g_policy = 0;
 enum ProfKind {
   PK_GEMM_QKV = 0, PK_GEMM_OPROJ, PK_GEMM_FFN_UP, PK_GEMM_FFN_DOWN, PK_GEMM_AUTOSPLIT, PK_ATTN_CAUSAL,
   PK_ATTN_STAGE2, PK_RMSNORM, PK_TOKENIZE, PK_BLOCK_TAIL, PK_HEAD, PK_TRAIN, PK_TRAIN_ATTN, PK_TRAIN_ELEM,
+  PK_EMBEDDING, PK_EMBEDDING_GRAD,
   PK_COUNT
 };
 static const char* kProfNames[PK_COUNT] = {"gemm_qkv", "gemm_oproj_rms", "gemm_ffn_up_gelu", "gemm_ffn_down_rms",
                                            "gemm_autosplit", "attn_causal", "attn_stage2", "rmsnorm",
                                            "tokenize_events", "fused_oproj_ffn", "score_head",
-                                           "train_gemm", "train_attn_rows", "train_elementwise"};
+                                           "train_gemm", "train_attn_rows", "train_elementwise",
+                                           "embedding", "embedding_grad"};
 struct ProfRec {
   int kind;
   cudaEvent_t e0, e1;
@@ -2242,3 +2246,5 @@ extern "C" onetrans_status onetrans_tokenize_autosplit_static(const onetrans_mod
   return m->bf16 ? autosplit_impl<__nv_bfloat16>(m, feats, N, ns_tokens, scratch, kStaticScratchBytes, st, nullptr)
                  : autosplit_impl<float>(m, feats, N, ns_tokens, scratch, kStaticScratchBytes, st, nullptr);
 }
+
+#include "input_api.cuh"
