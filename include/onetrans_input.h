@@ -79,6 +79,68 @@ ONETRANS_API onetrans_status onetrans_embedding_backward_sparse(
     int32_t ids_bits, int64_t R, int64_t n_rows, int32_t width, float scale, void* uniq, float* rows,
     int32_t* n_uniq, void* ws, size_t ws_bytes, void* stream);
 
+/* -------------------------------------------------- routed event tokenizer --
+ * Event r stands for up to k behaviours: its token is the weighted sum of its
+ * behaviours' tokens,
+ *   token[r] = sum_j weights[r][j] * (W2_t GELU(W1_t e_r + b1_t) + b2_t + emb_t),
+ * t = types[r][j], with the per-behavior MLPs and type identifiers of the
+ * model (Wb1, bb1, Wb2, bb2, type_emb; GELU in its tanh form).  With k = 1
+ * and no weights this is onetrans_tokenize_events' function; that call
+ * computes every behaviour's MLP for every event, these sort the events by
+ * behaviour and compute each event's own.  UNSUPPORTED when the model has no
+ * behavior MLPs or no type_emb.  1 <= k <= 8, R * k <= 2^26. */
+
+/* Sorts the choices by behaviour into `plan` (a caller's buffer of
+ * ONETRANS_OP_ROUTE bytes, 256-byte aligned), which the two calls below read
+ * for the same R and k.  types [R, k] int32 (device): 0 .. n_behaviors-1, or
+ * -1 for a choice that is none (it takes no part; a row of them gives a zero
+ * token).  Any other id counts as -1 and sets the device status word (code
+ * 3).  A behaviour may occur twice in a row. */
+ONETRANS_API onetrans_status onetrans_route_events(const onetrans_model* m, const int32_t* types, int64_t R,
+                                                   int32_t k, void* plan, size_t plan_bytes, void* stream);
+
+/* tokens of R events.
+ *   events [R, event_dim] (mode's type); weights [R, k] float32 or NULL (1);
+ *   tokens (mode's type): row r at (r / rows_per_sample) * sample_ld +
+ *     (r % rows_per_sample) * d elements, so that the S rows of x0
+ *     [B, L_S + L_NS, d] are written in place (rows_per_sample = L_S,
+ *     sample_ld = (L_S + L_NS) * d); rows_per_sample >= R: rows one after
+ *     another.  Elements outside those rows are left as they were.
+ * A plan that onetrans_route_events did not make for this model's behaviours,
+ * R and k sets the device status word (code 3) and nothing is written.
+ * BF16 mode: the hidden row z is rounded to bf16 as the operand of the second
+ * product; sums are float32, the token is rounded once. */
+ONETRANS_API onetrans_status onetrans_tokenize_routed(const onetrans_model* m, const void* events,
+                                                      const float* weights, int64_t R, int32_t k, const void* plan,
+                                                      size_t plan_bytes, void* tokens, int64_t rows_per_sample,
+                                                      int64_t sample_ld, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of the behaviour weights (float32, each with its weight's shape;
+ * host arrays of n_behaviors device pointers, type_emb [n_behaviors, d]).
+ * Written, not accumulated. */
+typedef struct {
+  float* const* Wb1;
+  float* const* bb1;
+  float* const* Wb2;
+  float* const* bb2;
+  float* type_emb;
+} onetrans_event_grads;
+
+/* The gradient of onetrans_tokenize_routed for the upstream gradient dtokens
+ * (laid out like tokens; element type dtokens_mode: ONETRANS_FP32, as
+ * onetrans_forward_backward writes dx0, or in BF16 mode ONETRANS_BF16):
+ *   devents [R, event_dim] (mode's type) or NULL;
+ *   dweights [R, k] float32 or NULL (0 where a choice is none);
+ *   grads: every weight gradient (zeros for a behaviour without events).
+ * BF16 mode: float32 dtokens are rounded to bf16 as matrix operands; z and
+ * the pre-activation gradient enter their products as two bf16 terms (16
+ * bits of significand), so the weight gradients keep float32 quality.  R = 0
+ * writes the zeros of grads.  The plan is checked as above. */
+ONETRANS_API onetrans_status onetrans_tokenize_routed_backward(
+    const onetrans_model* m, const void* events, const float* weights, int64_t R, int32_t k, const void* plan,
+    size_t plan_bytes, const void* dtokens, int32_t dtokens_mode, int64_t rows_per_sample, int64_t sample_ld,
+    void* devents, float* dweights, const onetrans_event_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -80,3 +80,81 @@ def test_gradient_argument_errors():
     for kw in (dict(uniq=None), dict(uniq=FAKE + 8), dict(n=None), dict(n=FAKE + 4)):
         assert sparse(**kw) == ot.ERR_INVALID_ARG, kw
     assert dense(R=0, out=None) == ot.ERR_INVALID_ARG      # the zeros still have to go somewhere
+
+
+def event_grads(n, addr=FAKE):
+    g = ot.EventGrads()
+    keep = []
+    for f in ot._BEH_FIELDS:
+        arr = (ot.P * n)(*[addr + 256 * i for i in range(n)])
+        keep.append(arr)
+        setattr(g, f, ctypes.cast(arr, ot.PP))
+    g.type_emb = addr
+    return g, keep
+
+
+def test_routed_workspaces():
+    fm = FakeModel(n_beh=3, event_dim=64)
+    for op in (ot.OP_ROUTE, ot.OP_ROUTED, ot.OP_ROUTED_BACKWARD):
+        st, a = size_of(fm, op, 1000, 1)
+        st2, b = size_of(fm, op, 10_000, 1)
+        st3, c = size_of(fm, op, 10_000, 3)
+        assert st == st2 == st3 == ot.OK and 0 < a < b < c
+        assert size_of(fm, op, 10, 0)[0] == ot.ERR_SHAPE
+        assert size_of(fm, op, 10, 9)[0] == ot.ERR_SHAPE
+        assert size_of(fm, op, -1, 1)[0] == ot.ERR_SHAPE
+        assert size_of(fm, op, 2 ** 26, 2)[0] == ot.ERR_SHAPE
+        assert size_of(fm, op, 0, 1)[0] == ot.OK
+        assert size_of(FakeModel(), op, 10, 1)[0] == ot.ERR_UNSUPPORTED      # no behavior MLPs
+
+
+def test_routed_argument_errors():
+    fm = FakeModel(n_beh=3, event_dim=64)
+    d = fm.cfg.d_model
+    g, keep = event_grads(3)
+    base = dict(m=fm.h, types=FAKE, ev=FAKE, wt=None, R=8, k=2, plan=FAKE, pb=BIG, tok=FAKE, per=8, ld=8 * d, ws=FAKE, nb=BIG,
+                dm=ot.BF16, de=FAKE, dw=FAKE, g=ctypes.byref(g))
+
+    def route(**kw):
+        a = dict(base, **kw)
+        return ot.lib.onetrans_route_events(a["m"], a["types"], a["R"], a["k"], a["plan"], a["pb"], None)
+
+    def tokens(**kw):
+        a = dict(base, **kw)
+        return ot.lib.onetrans_tokenize_routed(a["m"], a["ev"], a["wt"], a["R"], a["k"], a["plan"], a["pb"], a["tok"],
+                                               a["per"], a["ld"], a["ws"], a["nb"], None)
+
+    def grad(**kw):
+        a = dict(base, **kw)
+        return ot.lib.onetrans_tokenize_routed_backward(a["m"], a["ev"], a["wt"], a["R"], a["k"], a["plan"], a["pb"],
+                                                        a["tok"], a["dm"], a["per"], a["ld"], a["de"], a["dw"], a["g"],
+                                                        a["ws"], a["nb"], None)
+
+    none = FakeModel()
+    for f in (route, tokens, grad):
+        assert f(m=None) == ot.ERR_INVALID_ARG
+        assert f(m=none.h) == ot.ERR_UNSUPPORTED
+        for kw in (dict(R=-1), dict(k=0), dict(k=9), dict(R=2 ** 26)):
+            assert f(**kw) == ot.ERR_SHAPE, kw
+        for kw in (dict(plan=None), dict(plan=FAKE + 16)):
+            assert f(**kw) == ot.ERR_INVALID_ARG, kw
+        assert f(pb=size_of(fm, ot.OP_ROUTE, 8, 2)[1] - 1) == ot.ERR_CAPACITY
+    assert route(R=0, types=None, plan=None) == ot.OK
+    assert route(types=None) == route(types=FAKE + 4) == ot.ERR_INVALID_ARG
+    assert tokens(R=0, ev=None, plan=None, tok=None, ws=None) == ot.OK
+    for f in (tokens, grad):
+        for kw in (dict(ev=None), dict(ev=FAKE + 2), dict(tok=None), dict(tok=FAKE + 8), dict(ws=None), dict(ws=FAKE + 16), dict(wt=FAKE + 4)):
+            assert f(**kw) == ot.ERR_INVALID_ARG, kw
+        for kw in (dict(per=0), dict(per=4, ld=4 * d - 1)):
+            assert f(**kw) == ot.ERR_SHAPE, kw
+    assert tokens(nb=size_of(fm, ot.OP_ROUTED, 8, 2)[1] - 1) == ot.ERR_CAPACITY
+    assert grad(nb=size_of(fm, ot.OP_ROUTED_BACKWARD, 8, 2)[1] - 1) == ot.ERR_CAPACITY
+    for kw in (dict(dm=2), dict(de=FAKE + 8), dict(dw=FAKE + 4), dict(g=None)):
+        assert grad(**kw) == ot.ERR_INVALID_ARG, kw
+    keep[2][1] = FAKE + 4
+    assert grad() == ot.ERR_INVALID_ARG
+    keep[2][1] = None
+    assert grad() == ot.ERR_INVALID_ARG
+    fp = FakeModel(n_beh=3, event_dim=64, mode=ot.FP32)
+    keep[2][1] = FAKE
+    assert grad(m=fp.h, dm=ot.BF16) == ot.ERR_UNSUPPORTED

@@ -41,7 +41,8 @@ SYMBOLS = (
 # declared in include/onetrans_input.h
 INPUT_SYMBOLS = (
     "onetrans_input_workspace_size", "onetrans_embedding_lookup", "onetrans_embedding_backward",
-    "onetrans_embedding_backward_sparse",
+    "onetrans_embedding_backward_sparse", "onetrans_route_events", "onetrans_tokenize_routed",
+    "onetrans_tokenize_routed_backward",
 )
 
 
@@ -89,6 +90,11 @@ class Weights(ctypes.Structure):
                 + [(f, PP) for f in _BEH_FIELDS] + [("type_emb", P)] + [(f, P) for f in _HEAD_FIELDS])
 
 
+class EventGrads(ctypes.Structure):
+    """onetrans_event_grads: per-behavior host arrays of float32 device pointers."""
+    _fields_ = [(f, PP) for f in _BEH_FIELDS] + [("type_emb", P)]
+
+
 class Grads(ctypes.Structure):
     """onetrans_grads: per-layer host arrays of float32 device pointers."""
     _fields_ = [(f, PP) for f in _WEIGHT_FIELDS]
@@ -126,6 +132,9 @@ _sig("onetrans_embedding_lookup", I32, P, P, I32, I64, I32, P, I32, I64, ctypes.
 _sig("onetrans_embedding_backward", I32, P, P, I32, I64, P, I32, I64, I64, I32, ctypes.c_float, P, P, SZ, P)
 _sig("onetrans_embedding_backward_sparse", I32, P, P, I32, I64, P, I32, I64, I64, I32, ctypes.c_float, P, P, P, P, SZ,
      P)
+_sig("onetrans_route_events", I32, P, P, I64, I32, P, SZ, P)
+_sig("onetrans_tokenize_routed", I32, P, P, P, I64, I32, P, SZ, P, I64, I64, P, SZ, P)
+_sig("onetrans_tokenize_routed_backward", I32, P, P, P, I64, I32, P, SZ, P, I32, I64, I64, P, P, P, P, SZ, P)
 _sig("onetrans_set_kernel_policy", I32, I32)
 _sig("onetrans_device_status", I32, P, PI32)
 _sig("onetrans_selftest_bounded_wait", I32, I32, P)
@@ -525,3 +534,88 @@ def onetrans_embedding_backward_sparse(model: Model, dout: torch.Tensor, ids: to
     _check("onetrans_embedding_backward_sparse", lib.onetrans_embedding_backward_sparse(
         model.handle, _ptr(dout), _MODE_OF[dout.dtype], ld, _ptr(ids), _ID_BITS[ids.dtype], ids.shape[0], n_rows, w,
         scale, _ptr(uniq), _ptr(rows), _ptr(n_uniq), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def _choices(types: torch.Tensor):
+    """(R, k) of a types tensor [R] or [R, k]."""
+    _need(types.dim() in (1, 2) and types.is_contiguous() and types.dtype == torch.int32,
+          "types must be a contiguous int32 tensor [R] or [R, k]")
+    return types.shape[0], types.shape[1] if types.dim() == 2 else 1
+
+
+def _token_rows(t: torch.Tensor, R: int, d: int, what: str):
+    """(rows per sample, sample stride) of token rows [R, d] or [B, L, d] with R = B * L, the rows of a sample
+    one after another (a slice x0[:, :L_S] of contiguous x0 is taken in place)."""
+    _need(t.dim() in (2, 3) and t.shape[-1] == d, f"{what} must be [R, d] or [B, L, d]")
+    L = t.shape[-2]
+    _need((t.dim() == 2 and L == R) or (t.dim() == 3 and t.shape[0] * L == R), f"{what}: one row per event")
+    _need((d == 1 or t.stride(-1) == 1) and (L <= 1 or t.stride(-2) == d), f"{what}: a sample's rows must be contiguous")
+    if t.dim() == 2 or t.shape[0] <= 1:
+        return max(R, 1), max(R, 1) * d
+    _need(t.stride(0) >= L * d, f"{what}: samples overlap")
+    return max(L, 1), t.stride(0)
+
+
+def _routed_args(model: Model, events, types, weights, plan, ws, *more):
+    _on_one_device(events, types, weights, plan, ws, *more)
+    R, k = _choices(types)
+    e = model.cfg.event_dim
+    _need(events.dim() == 2 and tuple(events.shape) == (R, e) and events.is_contiguous() and events.dtype == model.dtype,
+          "events must be a contiguous [R, event_dim] tensor of the model dtype")
+    _need(weights is None or (weights.numel() == R * k and weights.is_contiguous() and weights.dtype == torch.float32),
+          "weights must be a contiguous float32 tensor of the types' shape, or None")
+    return R, k
+
+
+def onetrans_route_events(model: Model, types: torch.Tensor, plan: torch.Tensor, stream=None) -> None:
+    """Sorts the events' choices types [R] or [R, k] int32 (-1: none) by behaviour into plan
+    (model.input_workspace(OP_ROUTE, R, k))."""
+    _on_one_device(types, plan)
+    R, k = _choices(types)
+    _check("onetrans_route_events", lib.onetrans_route_events(model.handle, _ptr(types), R, k, _ptr(plan), plan.numel(),
+                                                              _stream(stream)))
+
+
+def onetrans_tokenize_routed(model: Model, events: torch.Tensor, types: torch.Tensor, weights: Optional[torch.Tensor],
+                             plan: torch.Tensor, tokens: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Tokens of events [R, event_dim] by the plan made from types; weights [R, k] float32 or None; tokens [R, d]
+    or [B, L_S, d] (may be the slice x0[:, :L_S]) of the model dtype."""
+    R, k = _routed_args(model, events, types, weights, plan, ws, tokens)
+    _need(tokens.dtype == model.dtype, "tokens must be of the model dtype")
+    per, ld = _token_rows(tokens, R, model.d, "tokens")
+    _check("onetrans_tokenize_routed", lib.onetrans_tokenize_routed(
+        model.handle, _ptr(events), _ptr(weights), R, k, _ptr(plan), plan.numel(), _ptr(tokens), per, ld, _ptr(ws),
+        ws.numel(), _stream(stream)))
+
+
+def onetrans_tokenize_routed_backward(model: Model, events: torch.Tensor, types: torch.Tensor,
+                                      weights: Optional[torch.Tensor], plan: torch.Tensor, dtokens: torch.Tensor,
+                                      devents: Optional[torch.Tensor], dweights: Optional[torch.Tensor], grads: Dict,
+                                      ws: torch.Tensor, stream=None) -> None:
+    """dtokens as tokens, float32 or the model dtype; devents [R, event_dim] (model dtype) or None; dweights
+    [R, k] float32 or None; grads maps Wb1, bb1, Wb2, bb2 to per-behavior lists of float32 tensors of the
+    weights' shapes and type_emb to a float32 tensor [n_behaviors, d]."""
+    R, k = _routed_args(model, events, types, weights, plan, ws, dtokens, devents, dweights, grads["type_emb"])
+    _need(dtokens.dtype in (model.dtype, torch.float32), "dtokens must be float32 or of the model dtype")
+    per, ld = _token_rows(dtokens, R, model.d, "dtokens")
+    _need(devents is None or (devents.shape == events.shape and devents.is_contiguous() and devents.dtype == model.dtype),
+          "devents must be a contiguous tensor like events, or None")
+    _need(dweights is None or (dweights.numel() == R * k and dweights.is_contiguous() and dweights.dtype == torch.float32),
+          "dweights must be a contiguous float32 tensor of the types' shape, or None")
+    T, d, e = model.cfg.n_behaviors, model.d, model.cfg.event_dim
+    g = EventGrads()
+    keep = []
+    for f, n in (("Wb1", d * e), ("bb1", d), ("Wb2", d * d), ("bb2", d)):
+        ts = grads[f]
+        _need(len(ts) == T and all(t.numel() == n and t.is_contiguous() and t.dtype == torch.float32 and t.is_cuda for t in ts),
+              f"grads['{f}'] must hold one contiguous float32 tensor of the weight's shape per behavior")
+        arr = (P * T)(*[t.data_ptr() for t in ts])
+        keep.append(arr)
+        setattr(g, f, ctypes.cast(arr, PP))
+    emb = grads["type_emb"]
+    _need(emb.numel() == T * d and emb.is_contiguous() and emb.dtype == torch.float32, "grads['type_emb'] must be float32 [n_behaviors, d]")
+    g.type_emb = emb.data_ptr()
+    _check("onetrans_tokenize_routed_backward", lib.onetrans_tokenize_routed_backward(
+        model.handle, _ptr(events), _ptr(weights), R, k, _ptr(plan), plan.numel(), _ptr(dtokens),
+        _MODE_OF[dtokens.dtype], per, ld, _ptr(devents), _ptr(dweights), ctypes.byref(g), _ptr(ws), ws.numel(),
+        _stream(stream)))

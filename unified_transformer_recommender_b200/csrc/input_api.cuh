@@ -196,6 +196,200 @@ static onetrans_status emb_grad_run(const EmbGrad& g, void* ws, size_t ws_bytes,
                           : emb_grad_impl<int64_t>(g, ws, ws_bytes, st, nullptr);
 }
 
+// ------------------------------------------------------- routed tokenizer --
+static const long long kMaxChoicesTotal = 1LL << 26;   // R * k
+
+// The plan in the caller's buffer.
+struct PlanBuf {
+  int* head;
+  int* order;
+  int* pos;
+  int* counts;       // per tile, while the plan is made
+  long long cap;     // slots: every choice, each behaviour filled up to 128
+  int tiles;
+  size_t bytes;
+};
+static PlanBuf plan_buf(const onetrans_model* m, void* base, long long R, int k) {
+  PlanBuf p;
+  const long long n = R * k;
+  Carve cv(base, 0);
+  p.cap = cdiv(n, 128) * 128 + 128LL * m->cfg.n_behaviors;
+  p.tiles = (int)cdiv(n, kRouteTile);
+  p.head = (int*)cv.take(kPlanHeader * sizeof(int));
+  p.order = (int*)cv.take((size_t)p.cap * sizeof(int));
+  p.pos = (int*)cv.take((size_t)n * sizeof(int));
+  p.counts = (int*)cv.take((size_t)p.tiles * kMaxTypes * sizeof(int));
+  p.bytes = cv.used;
+  return p;
+}
+static PlanView plan_view(const onetrans_model* m, const PlanBuf& p, long long R, int k) {
+  return PlanView{p.head, p.order, p.pos, (int)R, k, m->cfg.n_behaviors};
+}
+
+static bool has_behavior_mlps(const onetrans_model* m) {
+  if (m->cfg.n_behaviors < 1 || m->cfg.event_dim < 1 || m->Wb1.empty() || !m->type_emb) return false;
+  return true;
+}
+
+// What every call on routed events checks: the model, the sizes, and the
+// behaviour weights' pointers (model_create leaves those unchecked).
+static onetrans_status routed_check(const onetrans_model* m, long long R, int k) {
+  if (!m) return ONETRANS_ERR_INVALID_ARG;
+  if (!has_behavior_mlps(m)) return ONETRANS_ERR_UNSUPPORTED;
+  if (R < 0 || k < 1 || k > kMaxChoices || R > kMaxChoicesTotal / k) return ONETRANS_ERR_SHAPE;
+  for (int t = 0; t < m->cfg.n_behaviors; ++t)
+    for (const void* p : {m->Wb1[t], m->bb1[t], m->Wb2[t], m->bb2[t]})
+      if (!p || !aligned(p, 16)) return ONETRANS_ERR_INVALID_ARG;
+  if (!aligned(m->type_emb, 16)) return ONETRANS_ERR_INVALID_ARG;
+  return ONETRANS_OK;
+}
+static onetrans_status token_rows_check(const onetrans_model* m, long long R, long long per, long long sample_ld) {
+  if (per < 1 || per > 0x7fffffff || (R > per && sample_ld < per * m->d)) return ONETRANS_ERR_SHAPE;
+  return ONETRANS_OK;
+}
+
+static RoutedMLP routed_mlp_of(const onetrans_model* m) {
+  RoutedMLP w;
+  std::memset(&w, 0, sizeof(w));
+  for (int t = 0; t < m->cfg.n_behaviors; ++t) {
+    w.W1[t] = m->Wb1[t]; w.b1[t] = m->bb1[t]; w.W2[t] = m->Wb2[t]; w.b2[t] = m->bb2[t];
+  }
+  w.emb = m->type_emb;
+  return w;
+}
+
+static onetrans_status route_impl(const onetrans_model* m, const int32_t* types, long long R, int k, const PlanBuf& p,
+                                  cudaStream_t st) {
+  const int n = (int)(R * k), T = m->cfg.n_behaviors;
+  ProfScope prof(PK_ROUTE, 0.0, (double)n * 12, st);
+  if (p.tiles > 1)
+    launch_dependent(route_count_kernel, dim3(p.tiles), dim3(kRouteThreads), 0, st, types, n, T, p.counts);
+  launch_dependent(route_place_kernel, dim3(p.tiles), dim3(kRouteThreads), 0, st, types, n, (int)R, k, T,
+                   (const int*)p.counts, p.head, p.order, p.pos);
+  return last_launch();
+}
+
+template <typename T>
+static onetrans_status combine_launch(const PlanView& plan, const float* part, int width, void* out,
+                                      const TokenRows& rows, cudaStream_t st) {
+  const long long items = (long long)plan.R * width;
+  launch_dependent(routed_combine_kernel<T>, dim3((unsigned)std::min<long long>(cdiv(items, 256), 148 * 8)), dim3(256), 0,
+                   st, plan, part, width, (T*)out, rows);
+  return last_launch();
+}
+
+struct RoutedCall {
+  const void* events;
+  const float* weights;
+  long long R;
+  int k;
+  const PlanBuf* plan;
+  void* tokens;           // forward
+  const void* dtokens;    // backward
+  int dtokens_mode;
+  TokenRows rows;
+  void* devents;
+  float* dweights;
+  RoutedGrads grads;
+};
+
+template <typename T>
+static onetrans_status tokenize_routed_impl(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
+                                            size_t ws_bytes, cudaStream_t st, size_t* need) {
+  const int d = m->d, e = m->cfg.event_dim;
+  const long long cap = plan_buf(m, nullptr, R, k).cap;
+  Carve cv(ws, ws_bytes);
+  float* part = k > 1 ? (float*)cv.take((size_t)R * k * d * 4) : nullptr;
+  float* hidden = (float*)cv.take((size_t)cap * d * 4);
+  if (need) {
+    *need = cv.used;
+    return ONETRANS_OK;
+  }
+  if (cv.overflow) return ONETRANS_ERR_CAPACITY;
+  RoutedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.plan = plan_view(m, *c->plan, R, k);
+  a.mlp = routed_mlp_of(m);
+  a.e = e; a.d = d;
+  a.events = c->events; a.weights = c->weights; a.tokens = c->tokens; a.rows = c->rows;
+  a.buf0 = hidden; a.part = part;
+  ProfScope prof(PK_ROUTED, 2.0 * R * k * ((double)e * d + (double)d * d), (double)R * (e + d) * m->es, st);
+  const dim3 grid((unsigned)cdiv(d, 64), (unsigned)(cap / 64));
+  launch_dependent(routed_simt_kernel<T, T, RS_HIDDEN>, grid, dim3(256), 0, st, a);
+  launch_dependent(routed_simt_kernel<T, T, RS_TOKEN>, grid, dim3(256), 0, st, a);
+  OT_TRY(last_launch());
+  return combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st);
+}
+
+// Slices of the weight gradients: enough CTAs for the GPU's 148 SMs, no more
+// pieces than tiles.
+static int weight_slices(long long tiles, int blocks, int waves) {
+  return (int)std::max<long long>(1, std::min<long long>(tiles, cdiv(148 * waves, blocks)));
+}
+
+template <typename T, typename Td>
+static onetrans_status routed_backward_simt(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
+                                            size_t ws_bytes, cudaStream_t st, size_t* need) {
+  const int d = m->d, e = m->cfg.event_dim, T_n = m->cfg.n_behaviors;
+  const long long cap = plan_buf(m, nullptr, R, k).cap, tiles = cap / 128;
+  const int nb = (int)cdiv(d, 64), eb = (int)cdiv(e, 64);
+  const int n2 = nb * nb, n1 = nb * eb;
+  WeightPieces w;
+  w.slices = weight_slices(tiles, n2 + n1, 4);
+  w.per = (int)cdiv(tiles, w.slices);
+  w.stride = (long long)d * d + (long long)d * e + 2 * d;
+  Carve cv(ws, ws_bytes);
+  RoutedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.part = k > 1 ? (float*)cv.take((size_t)R * k * e * 4) : nullptr;
+  a.buf0 = (float*)cv.take((size_t)cap * d * 4);
+  a.buf1 = (float*)cv.take((size_t)cap * d * 4);
+  a.dot = (float*)cv.take((size_t)cap * nb * 4);
+  w.part = (float*)cv.take((size_t)(w.slices + T_n) * w.stride * 4);
+  if (need) {
+    *need = cv.used;
+    return ONETRANS_OK;
+  }
+  if (cv.overflow) return ONETRANS_ERR_CAPACITY;
+  a.plan = plan_view(m, *c->plan, R, k);
+  a.mlp = routed_mlp_of(m);
+  a.e = e; a.d = d;
+  a.events = c->events; a.weights = c->weights; a.dtokens = c->dtokens; a.rows = c->rows; a.devents = c->devents;
+  ProfScope prof(PK_ROUTED_GRAD, 2.0 * R * k * (3.0 * e * d + 2.0 * d * d), (double)R * (2 * e + d) * m->es, st);
+  const unsigned gy = (unsigned)(cap / 64);
+  launch_dependent(routed_simt_kernel<T, Td, RS_HIDDEN_GRAD>, dim3(nb, gy), dim3(256), 0, st, a);
+  launch_dependent(routed_simt_kernel<T, Td, RS_DU>, dim3(nb, gy), dim3(256), 0, st, a);
+  launch_dependent(routed_wgrad_simt_kernel<T, Td>, dim3(n2 + n1, w.slices), dim3(256), 0, st, a, w, n2);
+  launch_dependent(routed_wsum_kernel, dim3((unsigned)std::min<long long>(cdiv(w.stride, 256), 1024), T_n), dim3(256),
+                   0, st, a.plan, w, d, e, c->grads);
+  OT_TRY(last_launch());
+  if (c->devents) {
+    launch_dependent(routed_simt_kernel<T, Td, RS_DEVENT>, dim3(eb, gy), dim3(256), 0, st, a);
+    OT_TRY(last_launch());
+    OT_TRY(combine_launch<T>(a.plan, a.part, e, c->devents, TokenRows{0x7fffffff, 0}, st));
+  }
+  if (c->dweights) {
+    launch_dependent(routed_dweight_kernel<T, Td>, dim3((unsigned)std::min<long long>(cdiv(R * k, 8), 148 * 8)),
+                     dim3(256), 0, st, a.plan, a.mlp, d, (const Td*)c->dtokens, c->rows, (const float*)a.dot, nb,
+                     c->dweights);
+    OT_TRY(last_launch());
+  }
+  return ONETRANS_OK;
+}
+
+static onetrans_status tokenize_routed_any(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
+                                           size_t ws_bytes, cudaStream_t st, size_t* need) {
+  return m->bf16 ? tokenize_routed_impl<__nv_bfloat16>(m, c, R, k, ws, ws_bytes, st, need)
+                 : tokenize_routed_impl<float>(m, c, R, k, ws, ws_bytes, st, need);
+}
+static onetrans_status routed_backward_any(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
+                                           size_t ws_bytes, cudaStream_t st, size_t* need) {
+  const bool f32 = c && c->dtokens_mode == ONETRANS_FP32;
+  if (!m->bf16) return routed_backward_simt<float, float>(m, c, R, k, ws, ws_bytes, st, need);
+  return f32 ? routed_backward_simt<__nv_bfloat16, float>(m, c, R, k, ws, ws_bytes, st, need)
+             : routed_backward_simt<__nv_bfloat16, __nv_bfloat16>(m, c, R, k, ws, ws_bytes, st, need);
+}
+
 // ============================================================== C ABI ====
 extern "C" {
 
@@ -213,6 +407,16 @@ onetrans_status onetrans_input_workspace_size(const onetrans_model* m, int32_t o
       g.width = L;
       return emb_grad_impl<int32_t>(g, nullptr, 0, nullptr, bytes);
     }
+    case ONETRANS_OP_ROUTE:
+      OT_TRY(routed_check(m, n, L));
+      *bytes = plan_buf(m, nullptr, n, L).bytes;
+      return ONETRANS_OK;
+    case ONETRANS_OP_ROUTED:
+      OT_TRY(routed_check(m, n, L));
+      return tokenize_routed_any(m, nullptr, n, L, nullptr, 0, nullptr, bytes);
+    case ONETRANS_OP_ROUTED_BACKWARD:
+      OT_TRY(routed_check(m, n, L));
+      return routed_backward_any(m, nullptr, n, L, nullptr, 0, nullptr, bytes);
     default:
       return ONETRANS_ERR_INVALID_ARG;
   }
@@ -261,6 +465,81 @@ onetrans_status onetrans_embedding_backward_sparse(const onetrans_model* m, cons
   if (R == 0) return cuda_ok(cudaMemsetAsync(n_uniq, 0, sizeof(int32_t), (cudaStream_t)stream));
   if (!uniq || !rows || !aligned(uniq, 16) || !aligned(rows, 16)) return ONETRANS_ERR_INVALID_ARG;
   return emb_grad_run(g, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+onetrans_status onetrans_route_events(const onetrans_model* m, const int32_t* types, int64_t R, int32_t k, void* plan,
+                                      size_t plan_bytes, void* stream) {
+  OT_TRY(routed_check(m, R, k));
+  if (R == 0) return ONETRANS_OK;
+  if (!types || !plan || !aligned(types, 16) || !aligned(plan, 256)) return ONETRANS_ERR_INVALID_ARG;
+  const PlanBuf p = plan_buf(m, plan, R, k);
+  if (p.bytes > plan_bytes) return ONETRANS_ERR_CAPACITY;
+  return route_impl(m, types, R, k, p, (cudaStream_t)stream);
+}
+
+onetrans_status onetrans_tokenize_routed(const onetrans_model* m, const void* events, const float* weights, int64_t R,
+                                         int32_t k, const void* plan, size_t plan_bytes, void* tokens,
+                                         int64_t rows_per_sample, int64_t sample_ld, void* ws, size_t ws_bytes,
+                                         void* stream) {
+  OT_TRY(routed_check(m, R, k));
+  OT_TRY(token_rows_check(m, R, rows_per_sample, sample_ld));
+  if (R == 0) return ONETRANS_OK;
+  if (!events || !plan || !tokens || !ws || !aligned(events, 16) || !aligned(weights, 16) || !aligned(plan, 256) ||
+      !aligned(tokens, 16) || !aligned(ws, 256))
+    return ONETRANS_ERR_INVALID_ARG;
+  const PlanBuf p = plan_buf(m, const_cast<void*>(plan), R, k);
+  if (p.bytes > plan_bytes) return ONETRANS_ERR_CAPACITY;
+  RoutedCall c;
+  std::memset(&c, 0, sizeof(c));
+  c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
+  c.tokens = tokens;
+  c.rows = TokenRows{(int)rows_per_sample, sample_ld};
+  return tokenize_routed_any(m, &c, R, k, ws, ws_bytes, (cudaStream_t)stream, nullptr);
+}
+
+onetrans_status onetrans_tokenize_routed_backward(const onetrans_model* m, const void* events, const float* weights,
+                                                  int64_t R, int32_t k, const void* plan, size_t plan_bytes,
+                                                  const void* dtokens, int32_t dtokens_mode, int64_t rows_per_sample,
+                                                  int64_t sample_ld, void* devents, float* dweights,
+                                                  const onetrans_event_grads* grads, void* ws, size_t ws_bytes,
+                                                  void* stream) {
+  OT_TRY(routed_check(m, R, k));
+  if (!mode_ok(dtokens_mode)) return ONETRANS_ERR_INVALID_ARG;
+  if (!m->bf16 && dtokens_mode == ONETRANS_BF16) return ONETRANS_ERR_UNSUPPORTED;
+  OT_TRY(token_rows_check(m, R, rows_per_sample, sample_ld));
+  if (!grads || !grads->Wb1 || !grads->bb1 || !grads->Wb2 || !grads->bb2 || !grads->type_emb ||
+      !aligned(grads->type_emb, 16))
+    return ONETRANS_ERR_INVALID_ARG;
+  RoutedCall c;
+  std::memset(&c, 0, sizeof(c));
+  const int T = m->cfg.n_behaviors, d = m->d, e = m->cfg.event_dim;
+  for (int t = 0; t < T; ++t) {
+    c.grads.W1[t] = grads->Wb1[t]; c.grads.b1[t] = grads->bb1[t];
+    c.grads.W2[t] = grads->Wb2[t]; c.grads.b2[t] = grads->bb2[t];
+    for (const void* p : {(void*)c.grads.W1[t], (void*)c.grads.b1[t], (void*)c.grads.W2[t], (void*)c.grads.b2[t]})
+      if (!p || !aligned(p, 16)) return ONETRANS_ERR_INVALID_ARG;
+  }
+  c.grads.emb = grads->type_emb;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (R == 0) {   // no events: every gradient is zero
+    for (int t = 0; t < T; ++t) {
+      OT_TRY(cuda_ok(cudaMemsetAsync(c.grads.W1[t], 0, (size_t)d * e * 4, st)));
+      OT_TRY(cuda_ok(cudaMemsetAsync(c.grads.b1[t], 0, (size_t)d * 4, st)));
+      OT_TRY(cuda_ok(cudaMemsetAsync(c.grads.W2[t], 0, (size_t)d * d * 4, st)));
+      OT_TRY(cuda_ok(cudaMemsetAsync(c.grads.b2[t], 0, (size_t)d * 4, st)));
+    }
+    return cuda_ok(cudaMemsetAsync(c.grads.emb, 0, (size_t)T * d * 4, st));
+  }
+  if (!events || !plan || !dtokens || !ws || !aligned(events, 16) || !aligned(weights, 16) || !aligned(plan, 256) ||
+      !aligned(dtokens, 16) || !aligned(devents, 16) || !aligned(dweights, 16) || !aligned(ws, 256))
+    return ONETRANS_ERR_INVALID_ARG;
+  const PlanBuf p = plan_buf(m, const_cast<void*>(plan), R, k);
+  if (p.bytes > plan_bytes) return ONETRANS_ERR_CAPACITY;
+  c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
+  c.dtokens = dtokens; c.dtokens_mode = dtokens_mode;
+  c.rows = TokenRows{(int)rows_per_sample, sample_ld};
+  c.devents = devents; c.dweights = dweights;
+  return routed_backward_any(m, &c, R, k, ws, ws_bytes, st, nullptr);
 }
 
 }  // extern "C"

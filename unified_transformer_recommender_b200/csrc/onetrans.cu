@@ -23,6 +23,7 @@
 #include "attn_train.cuh"
 #include "gemm_wgrad.cuh"
 #include "embedding.cuh"
+#include "routed.cuh"
 
 using namespace ot;
 
@@ -57,14 +58,15 @@ static int g_policy = 0;
 enum ProfKind {
   PK_GEMM_QKV = 0, PK_GEMM_OPROJ, PK_GEMM_FFN_UP, PK_GEMM_FFN_DOWN, PK_GEMM_AUTOSPLIT, PK_ATTN_CAUSAL,
   PK_ATTN_STAGE2, PK_RMSNORM, PK_TOKENIZE, PK_BLOCK_TAIL, PK_HEAD, PK_TRAIN, PK_TRAIN_ATTN, PK_TRAIN_ELEM,
-  PK_EMBEDDING, PK_EMBEDDING_GRAD,
+  PK_EMBEDDING, PK_EMBEDDING_GRAD, PK_ROUTE, PK_ROUTED, PK_ROUTED_GRAD,
   PK_COUNT
 };
 static const char* kProfNames[PK_COUNT] = {"gemm_qkv", "gemm_oproj_rms", "gemm_ffn_up_gelu", "gemm_ffn_down_rms",
                                            "gemm_autosplit", "attn_causal", "attn_stage2", "rmsnorm",
                                            "tokenize_events", "fused_oproj_ffn", "score_head",
                                            "train_gemm", "train_attn_rows", "train_elementwise",
-                                           "embedding", "embedding_grad"};
+                                           "embedding", "embedding_grad", "route_events", "routed_tokens",
+                                           "routed_tokens_grad"};
 struct ProfRec {
   int kind;
   cudaEvent_t e0, e1;
