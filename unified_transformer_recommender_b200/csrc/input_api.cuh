@@ -278,6 +278,27 @@ static onetrans_status combine_launch(const PlanView& plan, const float* part, i
   return last_launch();
 }
 
+// Shapes the tensor-core kernels take.
+static bool routed_tc(const onetrans_model* m) {
+  const int d = m->d, e = m->cfg.event_dim;
+  return m->bf16 && d % 64 == 0 && d <= 384 && e % 16 == 0 && e <= 128;
+}
+static onetrans_status routed_maps(const onetrans_model* m, const RoutedMaps** out) {
+  std::lock_guard<std::mutex> lk(m->maps_mu);
+  if (!m->maps_made) {
+    const int d = m->d, e = m->cfg.event_dim;
+    for (int t = 0; t < kMaxTypes; ++t) {
+      const int u = std::min(t, m->cfg.n_behaviors - 1);
+      if (!make_tmap_3d(&m->maps.w1[t], m->Wb1[u], e, d, 1, e, (uint64_t)e * d, 64, 64, 1) ||
+          !make_tmap_3d(&m->maps.w2[t], m->Wb2[u], d, d, 1, d, (uint64_t)d * d, 64, d > 256 ? d / 2 : d, 1))
+        return ONETRANS_ERR_CUDA;
+    }
+    m->maps_made = true;
+  }
+  *out = &m->maps;
+  return ONETRANS_OK;
+}
+
 struct RoutedCall {
   const void* events;
   const float* weights;
@@ -298,8 +319,10 @@ static onetrans_status tokenize_routed_impl(const onetrans_model* m, const Route
                                             size_t ws_bytes, cudaStream_t st, size_t* need) {
   const int d = m->d, e = m->cfg.event_dim;
   const long long cap = plan_buf(m, nullptr, R, k).cap;
+  const bool tc = routed_tc(m) && g_policy == 0 && (!c || c->rows.sample_ld % 8 == 0);
   Carve cv(ws, ws_bytes);
   float* part = k > 1 ? (float*)cv.take((size_t)R * k * d * 4) : nullptr;
+  // the hidden rows of the CUDA-core kernels (sized for them whatever runs)
   float* hidden = (float*)cv.take((size_t)cap * d * 4);
   if (need) {
     *need = cv.used;
@@ -314,6 +337,26 @@ static onetrans_status tokenize_routed_impl(const onetrans_model* m, const Route
   a.events = c->events; a.weights = c->weights; a.tokens = c->tokens; a.rows = c->rows;
   a.buf0 = hidden; a.part = part;
   ProfScope prof(PK_ROUTED, 2.0 * R * k * ((double)e * d + (double)d * d), (double)R * (e + d) * m->es, st);
+  if (tc) {
+    const RoutedMaps* maps;
+    OT_TRY(routed_maps(m, &maps));
+    RoutedTcArgs ta;
+    std::memset(&ta, 0, sizeof(ta));
+    ta.plan = a.plan; ta.mlp = a.mlp; ta.e = e; ta.d = d;
+    ta.events = (const __nv_bfloat16*)c->events; ta.weights = c->weights;
+    ta.tokens = (__nv_bfloat16*)c->tokens; ta.rows = c->rows; ta.part = part;
+    const TokCfg cfg = tok_cfg(e, d);
+    const unsigned grid = (unsigned)std::min<long long>(cap / 128, device_sm_count());
+    if (k > 1) {
+      if (!allow_smem(routed_tokens_kernel<true>, cfg.smem)) return ONETRANS_ERR_CUDA;
+      launch_dependent(routed_tokens_kernel<true>, dim3(grid), dim3(kTokThreads), cfg.smem, st, *maps, ta);
+      OT_TRY(last_launch());
+      return combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st);
+    }
+    if (!allow_smem(routed_tokens_kernel<false>, cfg.smem)) return ONETRANS_ERR_CUDA;
+    launch_dependent(routed_tokens_kernel<false>, dim3(grid), dim3(kTokThreads), cfg.smem, st, *maps, ta);
+    return last_launch();
+  }
   const dim3 grid((unsigned)cdiv(d, 64), (unsigned)(cap / 64));
   launch_dependent(routed_simt_kernel<T, T, RS_HIDDEN>, grid, dim3(256), 0, st, a);
   launch_dependent(routed_simt_kernel<T, T, RS_TOKEN>, grid, dim3(256), 0, st, a);

@@ -24,6 +24,7 @@
 #include "gemm_wgrad.cuh"
 #include "embedding.cuh"
 #include "routed.cuh"
+#include "routed_tc.cuh"
 
 using namespace ot;
 
@@ -36,6 +37,11 @@ struct onetrans_model {
   std::vector<const void*> g_attn, g_ffn, Wqkv_S, Wqkv_NS, Wo, W1_S, b1_S, W2_S, b2_S, W1_NS,
       b1_NS, W2_NS, b2_NS, Wb1, bb1, Wb2, bb2;
   const void *Wa1, *ba1, *Wa2, *ba2, *type_emb, *w_head, *b_head;
+  // tensor maps of the behaviour MLPs, made by the first call that needs them
+  // (they depend on the weights' addresses and shapes alone)
+  mutable std::mutex maps_mu;
+  mutable bool maps_made = false;
+  mutable RoutedMaps maps;
 };
 
 struct onetrans_cache {
