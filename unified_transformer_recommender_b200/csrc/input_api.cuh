@@ -290,7 +290,7 @@ static onetrans_status routed_maps(const onetrans_model* m, const RoutedMaps** o
     for (int t = 0; t < kMaxTypes; ++t) {
       const int u = std::min(t, m->cfg.n_behaviors - 1);
       if (!make_tmap_3d(&m->maps.w1[t], m->Wb1[u], e, d, 1, e, (uint64_t)e * d, 64, 64, 1) ||
-          !make_tmap_3d(&m->maps.w2[t], m->Wb2[u], d, d, 1, d, (uint64_t)d * d, 64, d > 256 ? d / 2 : d, 1))
+          !make_tmap_3d(&m->maps.w2[t], m->Wb2[u], d, d, 1, d, (uint64_t)d * d, 64, 64, 1))
         return ONETRANS_ERR_CUDA;
     }
     m->maps_made = true;
@@ -420,6 +420,52 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   return ONETRANS_OK;
 }
 
+template <typename Td>
+static onetrans_status routed_backward_tc(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
+                                          size_t ws_bytes, cudaStream_t st, size_t* need) {
+  const int d = m->d, e = m->cfg.event_dim, T = m->cfg.n_behaviors;
+  const long long cap = plan_buf(m, nullptr, R, k).cap, tiles = cap / 128;
+  const WgCfg wc = wg_cfg(e, d);
+  WeightPieces w;
+  w.slices = (int)std::max<long long>(1, std::min<long long>(tiles, 148 / wc.roles));
+  w.per = (int)cdiv(tiles, w.slices);
+  w.stride = (long long)d * d + (long long)d * e + 2 * d;
+  Carve cv(ws, ws_bytes);
+  float* part = k > 1 ? (float*)cv.take((size_t)R * k * e * 4) : nullptr;
+  w.part = (float*)cv.take((size_t)(w.slices + T) * w.stride * 4);
+  if (need) {
+    *need = cv.used;
+    return ONETRANS_OK;
+  }
+  if (cv.overflow) return ONETRANS_ERR_CAPACITY;
+  const RoutedMaps* maps;
+  OT_TRY(routed_maps(m, &maps));
+  RoutedBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.plan = plan_view(m, *c->plan, R, k);
+  a.mlp = routed_mlp_of(m);
+  a.e = e; a.d = d;
+  a.events = (const __nv_bfloat16*)c->events; a.weights = c->weights; a.dtokens = c->dtokens; a.rows = c->rows;
+  a.devents = k == 1 ? (__nv_bfloat16*)c->devents : nullptr;
+  a.part = k > 1 && c->devents ? part : nullptr;
+  a.dweights = c->dweights;
+  ProfScope prof(PK_ROUTED_GRAD, 2.0 * R * k * (3.0 * e * d + 2.0 * d * d), (double)R * (2 * e + d) * m->es, st);
+  if (!allow_smem(routed_wgrad_kernel<Td>, wc.smem)) return ONETRANS_ERR_CUDA;
+  launch_dependent(routed_wgrad_kernel<Td>, dim3(wc.roles * w.slices), dim3(kTokThreads), wc.smem, st, *maps, a, w);
+  launch_dependent(routed_wsum_kernel, dim3((unsigned)std::min<long long>(cdiv(w.stride, 256), 1024), T), dim3(256), 0,
+                   st, a.plan, w, d, e, c->grads);
+  OT_TRY(last_launch());
+  if (c->devents || c->dweights) {
+    const DevCfg dc = dev_cfg(e, d);
+    if (!allow_smem(routed_devents_kernel<Td>, dc.smem)) return ONETRANS_ERR_CUDA;
+    launch_dependent(routed_devents_kernel<Td>, dim3((unsigned)std::min<long long>(tiles, device_sm_count())),
+                     dim3(kTokThreads), dc.smem, st, *maps, a);
+    OT_TRY(last_launch());
+  }
+  if (a.part) return combine_launch<__nv_bfloat16>(a.plan, part, e, c->devents, TokenRows{0x7fffffff, 0}, st);
+  return ONETRANS_OK;
+}
+
 static onetrans_status tokenize_routed_any(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
                                            size_t ws_bytes, cudaStream_t st, size_t* need) {
   return m->bf16 ? tokenize_routed_impl<__nv_bfloat16>(m, c, R, k, ws, ws_bytes, st, need)
@@ -429,6 +475,16 @@ static onetrans_status routed_backward_any(const onetrans_model* m, const Routed
                                            size_t ws_bytes, cudaStream_t st, size_t* need) {
   const bool f32 = c && c->dtokens_mode == ONETRANS_FP32;
   if (!m->bf16) return routed_backward_simt<float, float>(m, c, R, k, ws, ws_bytes, st, need);
+  if (routed_tc(m) && need) {   // whichever kernels the policy picks later
+    size_t tc = 0;
+    OT_TRY(routed_backward_tc<float>(m, nullptr, R, k, nullptr, 0, nullptr, &tc));
+    OT_TRY((routed_backward_simt<__nv_bfloat16, float>(m, nullptr, R, k, nullptr, 0, nullptr, need)));
+    *need = std::max(*need, tc);
+    return ONETRANS_OK;
+  }
+  if (routed_tc(m) && g_policy == 0 && c->rows.sample_ld % 8 == 0)
+    return f32 ? routed_backward_tc<float>(m, c, R, k, ws, ws_bytes, st, need)
+               : routed_backward_tc<__nv_bfloat16>(m, c, R, k, ws, ws_bytes, st, need);
   return f32 ? routed_backward_simt<__nv_bfloat16, float>(m, c, R, k, ws, ws_bytes, st, need)
              : routed_backward_simt<__nv_bfloat16, __nv_bfloat16>(m, c, R, k, ws, ws_bytes, st, need);
 }
