@@ -283,6 +283,19 @@ static bool routed_tc(const onetrans_model* m) {
   const int d = m->d, e = m->cfg.event_dim;
   return m->bf16 && d % 64 == 0 && d <= 384 && e % 16 == 0 && e <= 128;
 }
+// f(integral constant of d / 64)
+template <typename F>
+static onetrans_status by_chunks(int d, F f) {
+  switch (d / 64) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    default: return ONETRANS_ERR_UNSUPPORTED;
+  }
+}
 static onetrans_status routed_maps(const onetrans_model* m, const RoutedMaps** out) {
   std::lock_guard<std::mutex> lk(m->maps_mu);
   if (!m->maps_made) {
@@ -342,20 +355,21 @@ static onetrans_status tokenize_routed_impl(const onetrans_model* m, const Route
     OT_TRY(routed_maps(m, &maps));
     RoutedTcArgs ta;
     std::memset(&ta, 0, sizeof(ta));
-    ta.plan = a.plan; ta.mlp = a.mlp; ta.e = e; ta.d = d;
+    ta.plan = a.plan; ta.mlp = a.mlp; ta.e = e;
     ta.events = (const __nv_bfloat16*)c->events; ta.weights = c->weights;
     ta.tokens = (__nv_bfloat16*)c->tokens; ta.rows = c->rows; ta.part = part;
-    const TokCfg cfg = tok_cfg(e, d);
+    const int smem = tok_cfg(e, d).smem;
     const unsigned grid = (unsigned)std::min<long long>(cap / 128, device_sm_count());
-    if (k > 1) {
-      if (!allow_smem(routed_tokens_kernel<true>, cfg.smem)) return ONETRANS_ERR_CUDA;
-      launch_dependent(routed_tokens_kernel<true>, dim3(grid), dim3(kTokThreads), cfg.smem, st, *maps, ta);
-      OT_TRY(last_launch());
-      return combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st);
-    }
-    if (!allow_smem(routed_tokens_kernel<false>, cfg.smem)) return ONETRANS_ERR_CUDA;
-    launch_dependent(routed_tokens_kernel<false>, dim3(grid), dim3(kTokThreads), cfg.smem, st, *maps, ta);
-    return last_launch();
+    OT_TRY(by_chunks(d, [&](auto nc) {
+      constexpr int NC = decltype(nc)::value;
+      auto go = [&](auto kernel) {
+        if (!allow_smem(kernel, smem)) return ONETRANS_ERR_CUDA;
+        launch_dependent(kernel, dim3(grid), dim3(kTokThreads), smem, st, *maps, ta);
+        return last_launch();
+      };
+      return k > 1 ? go(routed_tokens_kernel<NC, true>) : go(routed_tokens_kernel<NC, false>);
+    }));
+    return k > 1 ? combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st) : ONETRANS_OK;
   }
   const dim3 grid((unsigned)cdiv(d, 64), (unsigned)(cap / 64));
   launch_dependent(routed_simt_kernel<T, T, RS_HIDDEN>, grid, dim3(256), 0, st, a);
@@ -420,7 +434,6 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   return ONETRANS_OK;
 }
 
-template <typename Td>
 static onetrans_status routed_backward_tc(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
                                           size_t ws_bytes, cudaStream_t st, size_t* need) {
   const int d = m->d, e = m->cfg.event_dim, T = m->cfg.n_behaviors;
@@ -433,6 +446,9 @@ static onetrans_status routed_backward_tc(const onetrans_model* m, const RoutedC
   Carve cv(ws, ws_bytes);
   float* part = k > 1 ? (float*)cv.take((size_t)R * k * e * 4) : nullptr;
   w.part = (float*)cv.take((size_t)(w.slices + T) * w.stride * 4);
+  // float32 dtokens as bf16 rows
+  __nv_bfloat16* rounded =
+      !c || c->dtokens_mode == ONETRANS_FP32 ? (__nv_bfloat16*)cv.take((size_t)R * d * 2) : nullptr;
   if (need) {
     *need = cv.used;
     return ONETRANS_OK;
@@ -440,30 +456,43 @@ static onetrans_status routed_backward_tc(const onetrans_model* m, const RoutedC
   if (cv.overflow) return ONETRANS_ERR_CAPACITY;
   const RoutedMaps* maps;
   OT_TRY(routed_maps(m, &maps));
-  RoutedBwdArgs a;
+  RoutedTcArgs a;
   std::memset(&a, 0, sizeof(a));
   a.plan = plan_view(m, *c->plan, R, k);
   a.mlp = routed_mlp_of(m);
-  a.e = e; a.d = d;
-  a.events = (const __nv_bfloat16*)c->events; a.weights = c->weights; a.dtokens = c->dtokens; a.rows = c->rows;
+  a.e = e;
+  a.events = (const __nv_bfloat16*)c->events; a.weights = c->weights;
+  a.dtokens = (const __nv_bfloat16*)c->dtokens; a.rows = c->rows;
   a.devents = k == 1 ? (__nv_bfloat16*)c->devents : nullptr;
   a.part = k > 1 && c->devents ? part : nullptr;
   a.dweights = c->dweights;
   ProfScope prof(PK_ROUTED_GRAD, 2.0 * R * k * (3.0 * e * d + 2.0 * d * d), (double)R * (2 * e + d) * m->es, st);
-  if (!allow_smem(routed_wgrad_kernel<Td>, wc.smem)) return ONETRANS_ERR_CUDA;
-  launch_dependent(routed_wgrad_kernel<Td>, dim3(wc.roles * w.slices), dim3(kTokThreads), wc.smem, st, *maps, a, w);
+  if (rounded) {
+    launch_dependent(routed_round_rows_kernel, dim3((unsigned)std::min<long long>(cdiv(R * (d / 8), 256), 148 * 8)),
+                     dim3(256), 0, st, (const float*)c->dtokens, c->rows, (int)R, d, rounded);
+    OT_TRY(last_launch());
+    a.dtokens = rounded;
+    a.rows = TokenRows{0x7fffffff, 0};
+  }
+  OT_TRY(by_chunks(d, [&](auto nc) {
+    constexpr int NC = decltype(nc)::value;
+    if (!allow_smem(routed_wgrad_kernel<NC>, wc.smem)) return ONETRANS_ERR_CUDA;
+    launch_dependent(routed_wgrad_kernel<NC>, dim3(wc.roles * w.slices), dim3(kWgThreads), wc.smem, st, *maps, a, w);
+    return last_launch();
+  }));
   launch_dependent(routed_wsum_kernel, dim3((unsigned)std::min<long long>(cdiv(w.stride, 256), 1024), T), dim3(256), 0,
                    st, a.plan, w, d, e, c->grads);
   OT_TRY(last_launch());
-  if (c->devents || c->dweights) {
-    const DevCfg dc = dev_cfg(e, d);
-    if (!allow_smem(routed_devents_kernel<Td>, dc.smem)) return ONETRANS_ERR_CUDA;
-    launch_dependent(routed_devents_kernel<Td>, dim3((unsigned)std::min<long long>(tiles, device_sm_count())),
-                     dim3(kTokThreads), dc.smem, st, *maps, a);
-    OT_TRY(last_launch());
-  }
-  if (a.part) return combine_launch<__nv_bfloat16>(a.plan, part, e, c->devents, TokenRows{0x7fffffff, 0}, st);
-  return ONETRANS_OK;
+  if (!c->devents && !c->dweights) return ONETRANS_OK;
+  const int smem = dev_cfg(e, d).smem;
+  OT_TRY(by_chunks(d, [&](auto nc) {
+    constexpr int NC = decltype(nc)::value;
+    if (!allow_smem(routed_devents_kernel<NC>, smem)) return ONETRANS_ERR_CUDA;
+    launch_dependent(routed_devents_kernel<NC>, dim3((unsigned)std::min<long long>(tiles, device_sm_count())),
+                     dim3(kTokThreads), smem, st, *maps, a);
+    return last_launch();
+  }));
+  return a.part ? combine_launch<__nv_bfloat16>(a.plan, part, e, c->devents, TokenRows{0x7fffffff, 0}, st) : ONETRANS_OK;
 }
 
 static onetrans_status tokenize_routed_any(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
@@ -477,14 +506,13 @@ static onetrans_status routed_backward_any(const onetrans_model* m, const Routed
   if (!m->bf16) return routed_backward_simt<float, float>(m, c, R, k, ws, ws_bytes, st, need);
   if (routed_tc(m) && need) {   // whichever kernels the policy picks later
     size_t tc = 0;
-    OT_TRY(routed_backward_tc<float>(m, nullptr, R, k, nullptr, 0, nullptr, &tc));
+    OT_TRY(routed_backward_tc(m, nullptr, R, k, nullptr, 0, nullptr, &tc));
     OT_TRY((routed_backward_simt<__nv_bfloat16, float>(m, nullptr, R, k, nullptr, 0, nullptr, need)));
     *need = std::max(*need, tc);
     return ONETRANS_OK;
   }
   if (routed_tc(m) && g_policy == 0 && c->rows.sample_ld % 8 == 0)
-    return f32 ? routed_backward_tc<float>(m, c, R, k, ws, ws_bytes, st, need)
-               : routed_backward_tc<__nv_bfloat16>(m, c, R, k, ws, ws_bytes, st, need);
+    return routed_backward_tc(m, c, R, k, ws, ws_bytes, st, need);
   return f32 ? routed_backward_simt<__nv_bfloat16, float>(m, c, R, k, ws, ws_bytes, st, need)
              : routed_backward_simt<__nv_bfloat16, __nv_bfloat16>(m, c, R, k, ws, ws_bytes, st, need);
 }

@@ -10,6 +10,7 @@
 #include <initializer_list>
 #include <mutex>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "common.cuh"
