@@ -36,6 +36,38 @@ __device__ inline void cp_async_commit() { asm volatile("cp.async.commit_group;"
 template <int N> __device__ inline void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ inline void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// The product warps run their loops with all 32 lanes and let one elected lane
+// issue: control flow and descriptors then stay warp-uniform, and the
+// descriptors in uniform registers, where the tensor-core instructions want
+// them (a branch on the lane number costs a register move per operand).
+// elect.sync picks the same lane every time, so a commit covers the products
+// that lane issued.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 // A slot of a ring and the parity of its current round.  Kept as a counter
 // pair: the product thread issues alone, and a division per step would cost
 // it as much as the products.
@@ -247,7 +279,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     }
   } else if (warp == 17) {
     // ------------------------------------------------------------- products
-    if (lane == 0) {
+    {
       const uint64_t dE = sdesc_k128(smem_u32(sE)), dW = sdesc_k128(smem_u32(sW));
       constexpr uint32_t id_u = idesc_bf16(128, 64);
       constexpr int n0 = d > 256 ? 256 : d, n1 = d - n0;
@@ -269,12 +301,12 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < ksteps)
-            umma_bf16(to, desc_add(de, (k >> 2) * 16384 + (k & 3) * 32), desc_add(dw, (k >> 2) * 8192 + (k & 3) * 32), id_u,
+            mma_ss(to, desc_add(de, (k >> 2) * 16384 + (k & 3) * 32), desc_add(dw, (k >> 2) * 8192 + (k & 3) * 32), id_u,
                       k ? 1u : 0u);
-        umma_commit(&u_full[gu & 1]);
+        mma_commit(&u_full[gu & 1]);
         if (++cu == NC) {
           cu = 0;
-          umma_commit(&e_empty[eu.s]);
+          mma_commit(&e_empty[eu.s]);
           eu.next(cfg.ebuf);
         }
         wu.next(cfg.stages);
@@ -291,15 +323,15 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {   // units 16k .. 16k+15 packed over U columns 16k .. 16k+7
           const uint32_t z = tU + (g & 1) * 64 + k * 16;
-          umma_bf16_ts(tD, z, desc_add(w2, k * 32), id_0, (cd | k) ? 1u : 0u);
-          if (n1) umma_bf16_ts(tD + n0, z, desc_add(w2, n0 * 128 + k * 32), id_1, (cd | k) ? 1u : 0u);
+          mma_ts(tD, z, desc_add(w2, k * 32), id_0, (cd | k) ? 1u : 0u);
+          if (n1) mma_ts(tD + n0, z, desc_add(w2, n0 * 128 + k * 32), id_1, (cd | k) ? 1u : 0u);
         }
-        umma_commit(&w_empty[wd.s]);
-        umma_commit(&dn_done[g & 1]);
+        mma_commit(&w_empty[wd.s]);
+        mma_commit(&dn_done[g & 1]);
         if (++cd == NC) {
           cd = 0;
           ++tiles_done;
-          umma_commit(d_full);
+          mma_commit(d_full);
         }
         wd.next(cfg.stages);
       }
@@ -583,7 +615,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     }
   } else if (warp == 17) {
     // ------------------------------------------------------------- products
-    if (lane == 0) {
+    {
       const uint64_t dA = sdesc_k128(smem_u32(sA)), dW1 = sdesc_k128(smem_u32(sW1));
       const uint64_t dW1t = sdesc_mn128(smem_u32(sW1), 8192), dW2t = sdesc_mn128(smem_u32(sW2), 8192);
       constexpr uint32_t id_u = idesc_bf16(128, 64), id_z = idesc_bf16(128, 64, false, true);
@@ -605,7 +637,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < ksteps)
-            umma_bf16(u, desc_add(da, d * 256 + (k >> 2) * 16384 + (k & 3) * 32),
+            mma_ss(u, desc_add(da, d * 256 + (k >> 2) * 16384 + (k & 3) * 32),
                       desc_add(dw, (k >> 2) * 8192 + (k & 3) * 32), id_u, k ? 1u : 0u);
 #pragma unroll
         for (int b = 0; b < NC; ++b) {       // 64 of the contraction per W2 unit
@@ -615,14 +647,14 @@ __global__ void __launch_bounds__(kTokThreads, 1)
           const uint64_t dz = desc_add(dW2t, w2.s * 8192);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_bf16(z, desc_add(da, b * 16384 + k * 32), desc_add(dz, k * 2048), id_z, (b | k) ? 1u : 0u);
-          umma_commit(&w2_empty[w2.s]);
+            mma_ss(z, desc_add(da, b * 16384 + k * 32), desc_add(dz, k * 2048), id_z, (b | k) ? 1u : 0u);
+          mma_commit(&w2_empty[w2.s]);
           w2.next(cfg.units);
         }
-        umma_commit(&u_full[gu & 1]);
+        mma_commit(&u_full[gu & 1]);
         if (++cu == NC) {
           cu = 0;
-          umma_commit(&a_empty[ar.s]);
+          mma_commit(&a_empty[ar.s]);
           ar.next(cfg.abuf);
         }
         w1u.next(kDevW1);
@@ -643,15 +675,15 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t du = tU + (g & 1) * 64 + k * 16;   // hi in 8 columns, lo in the next 8
-          umma_bf16_ts(to, du, desc_add(w1, k * 2048), id_e, (cd | k) ? 1u : 0u);
-          umma_bf16_ts(to, du + 8, desc_add(w1, k * 2048), id_e, 1u);
+          mma_ts(to, du, desc_add(w1, k * 2048), id_e, (cd | k) ? 1u : 0u);
+          mma_ts(to, du + 8, desc_add(w1, k * 2048), id_e, 1u);
         }
-        umma_commit(&w1_empty[w1d.s]);
-        umma_commit(&du_done[g & 1]);
+        mma_commit(&w1_empty[w1d.s]);
+        mma_commit(&du_done[g & 1]);
         w1d.next(kDevW1);
         if (++cd == NC) {
           cd = 0;
-          umma_commit(&de_full[i & 1]);
+          mma_commit(&de_full[i & 1]);
           ++i;
         }
         if (!same && g + 1 < total) up();
@@ -925,7 +957,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
   } else if (warp == 13) {
     // ------------------------------------------------------------- products
-    if (lane == 0) {
+    {
       const uint64_t dW1 = sdesc_k128(smem_u32(sW1)), dW2 = sdesc_mn128(smem_u32(sW2), d * 128);
       const uint64_t dSk = sdesc_k128(smem_u32(sS)), dSm = sdesc_mn128(smem_u32(sS), 8192);
       constexpr uint32_t id_u = idesc_bf16(128, 64), id_z = idesc_bf16(128, 64, true, false);
@@ -945,12 +977,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           const uint64_t rows = desc_add(dSm, sg.s * cfg.stage_bytes + d * 128);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            umma_bf16_ts(tW1, tZ + k * 16, desc_add(rows, k * 2048), id_1, fresh && !k ? 0u : 1u);
-            umma_bf16_ts(tW1, tZ + k * 16 + 8, desc_add(rows, k * 2048), id_1, 1u);
+            mma_ts(tW1, tZ + k * 16, desc_add(rows, k * 2048), id_1, fresh && !k ? 0u : 1u);
+            mma_ts(tW1, tZ + k * 16 + 8, desc_add(rows, k * 2048), id_1, 1u);
           }
         }
-        umma_commit(du_free);
-        umma_commit(&s_empty[sg.s]);
+        mma_commit(du_free);
+        mma_commit(&s_empty[sg.s]);
         sg.next(cfg.stages);
       };
       for (int t = 0; t < T && ok; ++t) {
@@ -970,9 +1002,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (k < ksteps)
-              umma_bf16(tU, desc_add(dW1, (k >> 2) * 16384 + (k & 3) * 32),
+              mma_ss(tU, desc_add(dW1, (k >> 2) * 16384 + (k & 3) * 32),
                         desc_add(rk, d * 128 + (k >> 2) * 8192 + (k & 3) * 32), id_u, k ? 1u : 0u);
-          umma_commit(u_full);
+          mma_commit(u_full);
           if (q > 0) {
             if (!early) grad1(i - 1, q == 1);
             ok = ok && mbar_wait(du_free, (i - 1) & 1);
@@ -982,8 +1014,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           if (do1) {
 #pragma unroll
             for (int k = 0; k < NC * 4; ++k)
-              umma_bf16(tZ, desc_add(dW2, k * 2048), desc_add(rk, (k >> 2) * 8192 + (k & 3) * 32), id_z, k ? 1u : 0u);
-            umma_commit(dz_full);
+              mma_ss(tZ, desc_add(dW2, k * 2048), desc_add(rk, (k >> 2) * 8192 + (k & 3) * 32), id_z, k ? 1u : 0u);
+            mma_commit(dz_full);
           }
           ok = mbar_wait(z_ready, i & 1);
           if (!ok) break;
@@ -992,20 +1024,20 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t z = tU + k * 16;
-              umma_bf16_ts(tW2, z, desc_add(rm, k * 2048), id_2, q || k ? 1u : 0u);
-              umma_bf16_ts(tW2, z + 8, desc_add(rm, k * 2048), id_2, 1u);
+              mma_ts(tW2, z, desc_add(rm, k * 2048), id_2, q || k ? 1u : 0u);
+              mma_ts(tW2, z + 8, desc_add(rm, k * 2048), id_2, 1u);
               if (n1) {
-                umma_bf16_ts(tW2 + n0, z, desc_add(rm, n0 * 128 + k * 2048), id_2b, q || k ? 1u : 0u);
-                umma_bf16_ts(tW2 + n0, z + 8, desc_add(rm, n0 * 128 + k * 2048), id_2b, 1u);
+                mma_ts(tW2 + n0, z, desc_add(rm, n0 * 128 + k * 2048), id_2b, q || k ? 1u : 0u);
+                mma_ts(tW2 + n0, z + 8, desc_add(rm, n0 * 128 + k * 2048), id_2b, 1u);
               }
             }
           }
-          umma_commit(z_free);
+          mma_commit(z_free);
         }
         if (!ok) break;
         grad1(i - 1, n == 1);
         ok = ok && mbar_wait(du_free, (i - 1) & 1);
-        umma_commit(acc_full);
+        mma_commit(acc_full);
         ++p;
       }
     }
