@@ -160,8 +160,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the raw handle: building a Stream object costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -468,16 +468,24 @@ def _on_one_device(*tensors: Optional[torch.Tensor]) -> None:
     """Every tensor on the current CUDA device, where the call's kernels run."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on the current CUDA device ({dev}), got one on {t.device}")
 
 
 def _rows(t: torch.Tensor, what: str):
-    """(leading dimension, width) of a 2-D tensor whose rows are contiguous."""
-    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), f"{what} must be 2-D with contiguous rows")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    _need(ld >= t.shape[1], f"{what}: rows overlap")
-    return ld, t.shape[1]
+    """(rows, leading dimension, width) of a 2-D tensor whose rows are contiguous and do not overlap."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(what + " must be 2-D")
+    R, w = shape
+    if t.is_contiguous():
+        return R, w, w
+    ld, st = t.stride()
+    if R <= 1:
+        ld = w
+    if (w > 1 and st != 1) or ld < w:
+        raise ValueError(what + " must have contiguous rows that do not overlap")
+    return R, ld, w
 
 
 def onetrans_embedding_lookup(model: Model, table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor,
@@ -485,22 +493,24 @@ def onetrans_embedding_lookup(model: Model, table: torch.Tensor, ids: torch.Tens
     """out[r] = scale * table[ids[r]]; id -1 gives a zero row.  table [V, w] bf16 or float32; ids [R] int32 or
     int64; out [R, w] of the model dtype, rows contiguous, any row stride."""
     _on_one_device(table, ids, out)
-    ld, w = _rows(out, "out")
-    _need(table.dim() == 2 and table.is_contiguous() and table.dtype in _MODE_OF,
-          "table must be a contiguous [V, w] tensor of bfloat16 or float32")
-    _need(ids.dim() == 1 and ids.is_contiguous() and ids.dtype in _ID_BITS,
-          "ids must be a contiguous [R] tensor of int32 or int64")
-    _need(out.dtype == model.dtype and out.shape[0] == ids.shape[0] and w == table.shape[1],
-          "out must be [R, w] of the model dtype")
-    _check("onetrans_embedding_lookup", lib.onetrans_embedding_lookup(
-        model.handle, _ptr(table), _MODE_OF[table.dtype], table.shape[0], w, _ptr(ids), _ID_BITS[ids.dtype],
-        ids.shape[0], scale, _ptr(out), ld, _stream(stream)))
+    R, ld, w = _rows(out, "out")
+    tm, bits, ts = _MODE_OF.get(table.dtype), _ID_BITS.get(ids.dtype), table.shape
+    if tm is None or len(ts) != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous [V, w] tensor of bfloat16 or float32")
+    if bits is None or ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous [R] tensor of int32 or int64")
+    if out.dtype != model.dtype or R != ids.shape[0] or w != ts[1]:
+        raise ValueError("out must be [R, w] of the model dtype")
+    s = lib.onetrans_embedding_lookup(model.handle, table.data_ptr(), tm, ts[0], w, ids.data_ptr(), bits, R, scale,
+                                      out.data_ptr(), ld, _stream(stream))
+    if s:
+        _check("onetrans_embedding_lookup", s)
 
 
 def _grad_args(dout: torch.Tensor, ids: torch.Tensor):
-    ld, w = _rows(dout, "dout")
+    R, ld, w = _rows(dout, "dout")
     _need(dout.dtype in _MODE_OF, "dout must be bfloat16 or float32")
-    _need(ids.dim() == 1 and ids.is_contiguous() and ids.dtype in _ID_BITS and ids.shape[0] == dout.shape[0],
+    _need(ids.dim() == 1 and ids.is_contiguous() and ids.dtype in _ID_BITS and ids.shape[0] == R,
           "ids must be a contiguous [R] tensor of int32 or int64, one id per row of dout")
     return ld, w
 

@@ -80,46 +80,44 @@ __device__ inline uint32_t emb_key(Id id, uint32_t n_rows) {
 }
 
 // ----------------------------------------------------------------- lookup --
-constexpr int kLookThreads = 256, kLookUnroll = 4;
+constexpr int kLookThreads = 256;
 
-// Each CTA takes `rows` output rows, each thread kLookUnroll groups of VE
-// columns per round: the ids of all groups are loaded before the first row
-// access, so that kLookUnroll row reads are in flight per thread.
-template <typename Tt, typename To, typename Id, int VE>
+// A thread keeps its group of VE columns (cpr of them a row, at most
+// kLookThreads) and walks U rows: the ids of all of them are loaded before the
+// first row, so that U row reads are in flight per thread.  Wider rows go
+// over in blocks of kLookThreads groups (blockIdx.y).
+template <typename Tt, typename To, typename Id, int VE, int U>
 __global__ void __launch_bounds__(kLookThreads) emb_lookup_kernel(const Tt* __restrict__ table, uint32_t n_rows,
                                                                   int width, const Id* __restrict__ ids, long long R,
-                                                                  int rows, float scale, To* __restrict__ out,
+                                                                  int cpr, float scale, To* __restrict__ out,
                                                                   long long out_ld) {
-  const int cpr = width / VE;
-  const long long r0 = (long long)blockIdx.x * rows;
-  const int items = (int)min((long long)rows, R - r0) * cpr;
+  const int rpb = kLookThreads / cpr, r = threadIdx.x / cpr;   // rows a CTA looks at together
+  const int col = (blockIdx.y * kLookThreads + threadIdx.x - r * cpr) * VE;
+  const long long r0 = (long long)blockIdx.x * rpb * U + r;
   grid_dep_wait();
   grid_dep_launch();
-  for (int i0 = threadIdx.x; i0 < items; i0 += kLookThreads * kLookUnroll) {
-    uint32_t key[kLookUnroll];
-    int row[kLookUnroll], col[kLookUnroll];
+  if (r >= rpb || col >= width) return;
+  uint32_t key[U];
 #pragma unroll
-    for (int u = 0; u < kLookUnroll; ++u) {
-      const int i = i0 + u * kLookThreads;
-      row[u] = i / cpr;
-      col[u] = (i - row[u] * cpr) * VE;
-      key[u] = i < items ? emb_key(ids[r0 + row[u]], n_rows) : n_rows;
+  for (int u = 0; u < U; ++u) key[u] = r0 + u * rpb < R ? emb_key(ids[r0 + u * rpb], n_rows) : n_rows;
+  float v[U][VE];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (key[u] < n_rows) {
+      emb_ld<VE>(table + (long long)key[u] * width + col, v[u]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) v[u][e] = 0.f;
     }
-    float v[kLookUnroll][VE];
+  }
+  To* o = out + r0 * out_ld + col;
 #pragma unroll
-    for (int u = 0; u < kLookUnroll; ++u) {
-      if (key[u] < n_rows) {
-        emb_ld<VE>(table + (long long)key[u] * width + col[u], v[u]);
+  for (int u = 0; u < U; ++u) {
+    if (r0 + u * rpb < R) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[u][e] *= scale;
-      } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) v[u][e] = 0.f;
-      }
+      for (int e = 0; e < VE; ++e) v[u][e] *= key[u] < n_rows ? scale : 0.f;
+      emb_st<VE>(o + (long long)u * rpb * out_ld, v[u]);
     }
-#pragma unroll
-    for (int u = 0; u < kLookUnroll; ++u)
-      if (i0 + u * kLookThreads < items) emb_st<VE>(out + (r0 + row[u]) * out_ld + col[u], v[u]);
   }
 }
 
@@ -131,8 +129,8 @@ __global__ void __launch_bounds__(kLookThreads) emb_lookup_kernel(const Tt* __re
 // pass are ready when it starts: the first pass's come from sort_hist_kernel,
 // a later pass's are added up, as integers, by the pass before it while it
 // scatters (a destination's tile is known there).
-constexpr int kSortThreads = 1024, kSortItems = 4, kSortTile = kSortThreads * kSortItems;
-constexpr int kSortWarps = kSortThreads / 32, kSortMaxBits = 11;
+constexpr int kSortThreads = 512, kSortItems = 4, kSortTile = kSortThreads * kSortItems;
+constexpr int kSortWarps = kSortThreads / 32, kSortMaxBits = 8;
 
 struct SortArgs {
   uint32_t n_rows;       // keys 0 .. n_rows
@@ -195,22 +193,24 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const Id* __res
 
 // hist[tile][digit] -> the digit's count in the tiles before, tot[digit] its
 // total.  One CTA per 32 digits, the tiles split among the warps.
-__global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(SortArgs a) {
-  __shared__ int part[kSortWarps][32];
+__global__ void __launch_bounds__(1024) sort_scan_kernel(SortArgs a) {
+  __shared__ int part[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << a.bits;
   const int b = blockIdx.x * 32 + lane;
-  const int per = (a.tiles + kSortWarps - 1) / kSortWarps;
+  const int per = (a.tiles + 31) / 32;
   const int t0 = min(a.tiles, warp * per), t1 = min(a.tiles, t0 + per);
   const bool on = b < bins;
   grid_dep_wait();
   grid_dep_launch();
   int s = 0;
-  if (on)
+  if (on) {
+#pragma unroll 4
     for (int t = t0; t < t1; ++t) s += a.hist[(long long)t * bins + b];
+  }
   part[warp][lane] = s;
   __syncthreads();
   int before = 0, all = 0;
-  for (int w = 0; w < kSortWarps; ++w) {
+  for (int w = 0; w < 32; ++w) {
     const int p = part[w][lane];
     if (w < warp) before += p;
     all += p;
@@ -281,29 +281,30 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const Id* __res
     val[u] = !on[u] ? 0u : FIRST ? (uint32_t)i : vals_in[i];
     digit[u] = (key[u] >> a.shift) & (bins - 1);
   }
-  // where the tile's items of each digit begin
-  int tot[2] = {0, 0}, mine[2] = {0, 0};
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int b = threadIdx.x * 2 + q;   // two neighbouring digits a thread (kSortMaxBits = 11)
-    if (b < bins) {
-      if (a.scanned) {
-        tot[q] = a.tot[b];
-        mine[q] = a.hist[(long long)blockIdx.x * bins + b];
-      } else {
+  // where the tile's items of each digit begin: two threads a digit (the
+  // even and the odd tiles), neighbouring lanes
+  static_assert(kSortThreads == 2 << kSortMaxBits, "two threads per digit");
+  const int b = threadIdx.x >> 1, odd = threadIdx.x & 1;
+  int tot = 0, mine = 0;
+  if (b < bins) {
+    if (a.scanned) {
+      if (!odd) {
+        tot = a.tot[b];
+        mine = a.hist[(long long)blockIdx.x * bins + b];
+      }
+    } else {
 #pragma unroll 8
-        for (int t = 0; t < a.tiles; ++t) {
-          const int c = a.hist[(long long)t * bins + b];
-          tot[q] += c;
-          if (t < (int)blockIdx.x) mine[q] += c;
-        }
+      for (int t = odd; t < a.tiles; t += 2) {
+        const int c = a.hist[(long long)t * bins + b];
+        tot += c;
+        if (t < (int)blockIdx.x) mine += c;
       }
     }
   }
+  mine += __shfl_xor_sync(~0u, mine, 1);
   int all;
-  const int ex = block_exclusive(tot[0] + tot[1], warp_sums, all);
-  if (threadIdx.x * 2 < bins) base[threadIdx.x * 2] = ex + mine[0];
-  if (threadIdx.x * 2 + 1 < bins) base[threadIdx.x * 2 + 1] = ex + tot[0] + mine[1];
+  const int ex = block_exclusive(tot, warp_sums, all);   // at the even thread: the digits before
+  if (b < bins && !odd) base[b] = ex + mine;
   int rank[kSortItems];
   sort_rank(digit, on, sort_sm, bins, rank);
 #pragma unroll
@@ -317,87 +318,48 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const Id* __res
   }
 }
 
-// Up to kSortTile ids in one CTA: every pass through shared memory.
+// Up to kRankMax ids: every id's place is the number of ids before it (smaller,
+// or equal and earlier), counted against all of them in shared memory, four
+// ids per warp.  One launch and one barrier where the radix sort takes a chain
+// of them; the R^2 comparisons are spread over the GPU.
+constexpr int kRankMax = 4096, kRankThreads = 256, kRankIds = 4;
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const Id* __restrict__ ids, uint32_t n_rows, int R,
-                                                                  int passes, int bits, uint32_t* __restrict__ keys,
-                                                                  uint32_t* __restrict__ vals, int* __restrict__ heads,
-                                                                  int chunk) {
-  extern __shared__ uint16_t sort_sm[];
-  __shared__ int warp_sums[32];
-  const int bins = 1 << bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int* base = (int*)(sort_sm + kSortWarps * bins);
-  uint32_t* sk = (uint32_t*)(base + max(bins, 32));   // [kSortTile] keys, then positions
-  uint32_t* sv = sk + kSortTile;
+__global__ void __launch_bounds__(kRankThreads) sort_rank_kernel(const Id* __restrict__ ids, uint32_t n_rows, int R,
+                                                                 uint32_t* __restrict__ keys,
+                                                                 uint32_t* __restrict__ vals) {
+  __shared__ __align__(16) uint32_t sk[kRankMax];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  uint32_t key[kSortItems], val[kSortItems], digit[kSortItems];
-  bool on[kSortItems];
-#pragma unroll
-  for (int u = 0; u < kSortItems; ++u) {
-    const int i = (warp * kSortItems + u) * 32 + lane;
-    on[u] = i < R;
-    key[u] = on[u] ? emb_key(ids[i], n_rows) : 0u;
-    val[u] = (uint32_t)i;
-  }
-  for (int p = 0; p < passes; ++p) {
-    for (int i = threadIdx.x; i < kSortWarps * bins / 2; i += kSortThreads) ((uint32_t*)sort_sm)[i] = 0;
-    for (int i = threadIdx.x; i < bins; i += kSortThreads) base[i] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kSortItems; ++u) {
-      digit[u] = (key[u] >> (p * bits)) & (bins - 1);
-      if (on[u]) atomicAdd(&base[digit[u]], 1);
-    }
-    int rank[kSortItems];
-    sort_rank(digit, on, sort_sm, bins, rank);   // its barriers also close the counts
-    const int b0 = threadIdx.x * 2;
-    const int c0 = b0 < bins ? base[b0] : 0, c1 = b0 + 1 < bins ? base[b0 + 1] : 0;
-    int all;
-    const int ex = block_exclusive(c0 + c1, warp_sums, all);
-    if (b0 < bins) base[b0] = ex;
-    if (b0 + 1 < bins) base[b0 + 1] = ex + c0;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kSortItems; ++u)
-      if (on[u]) {
-        const int to = base[digit[u]] + sort_sm[warp * bins + digit[u]] + rank[u];
-        sk[to] = key[u];
-        sv[to] = val[u];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kSortItems; ++u) {
-      const int i = (warp * kSortItems + u) * 32 + lane;
-      if (on[u]) {
-        key[u] = sk[i];
-        val[u] = sv[i];
-      }
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kSortItems; ++u) {
-    const int i = (warp * kSortItems + u) * 32 + lane;
-    if (on[u]) {
-      keys[i] = key[u];
-      vals[i] = val[u];
-    }
-  }
-  if (!heads) return;
-  // heads[c]: rows that begin in chunk c (chunk is a multiple of 32, and 32
-  // consecutive items are one warp's round)
-  __syncthreads();   // sk read by every warp
-  for (int i = threadIdx.x; i < (R + chunk - 1) / chunk; i += kSortThreads) base[i] = 0;
+  const int n4 = (R + 127) & ~127;     // whole rounds of 32 lanes x 4 keys
+  for (int i = threadIdx.x; i < n4; i += kRankThreads) sk[i] = i < R ? emb_key(ids[i], n_rows) : 0xffffffffu;
   __syncthreads();
+  const int i0 = (blockIdx.x * (kRankThreads / 32) + warp) * kRankIds;
+  if (i0 >= R) return;
+  uint32_t k[kRankIds];
+  int n[kRankIds];
 #pragma unroll
-  for (int u = 0; u < kSortItems; ++u) {
-    const int i = (warp * kSortItems + u) * 32 + lane;
-    const bool head = on[u] && key[u] < n_rows && (i == 0 || sk[i - 1] != key[u]);
-    const int n = __popc(__ballot_sync(~0u, head));
-    if (lane == 0 && n) atomicAdd(&base[i / chunk], n);
+  for (int u = 0; u < kRankIds; ++u) {
+    k[u] = sk[min(i0 + u, R - 1)];
+    n[u] = 0;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < (R + chunk - 1) / chunk; i += kSortThreads) heads[i] = base[i];
+  for (int j0 = lane * 4; j0 < n4; j0 += 128) {
+    const uint4 q = *(const uint4*)&sk[j0];
+#pragma unroll
+    for (int u = 0; u < kRankIds; ++u) {   // id j is before id i when key j < key i + (j < i)
+      const int i = i0 + u;
+      n[u] += (q.x < k[u] + (j0 < i)) + (q.y < k[u] + (j0 + 1 < i)) + (q.z < k[u] + (j0 + 2 < i)) +
+              (q.w < k[u] + (j0 + 3 < i));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRankIds; ++u) {
+    const int to = __reduce_add_sync(~0u, n[u]);
+    if (lane == u && i0 + u < R) {
+      keys[to] = k[u];
+      vals[to] = (uint32_t)(i0 + u);
+    }
+  }
 }
 
 // ----------------------------------------------------------------- reduce --
@@ -421,18 +383,19 @@ __global__ void __launch_bounds__(256) emb_heads_kernel(const uint32_t* __restri
   if (threadIdx.x == 0) heads[blockIdx.x] = sum;
 }
 
-constexpr int kRedWarps = 8, kRedBatch = 8;
+constexpr int kRedWarps = 8, kJoinWarps = 8;
 
 struct ReduceArgs {
   const uint32_t *keys, *vals;   // sorted
   uint32_t n_rows;
   long long R, dout_ld;
-  int width, chunk, chunks;      // chunk: sorted positions a CTA, a multiple of 32 * kRedWarps
+  int width, chunk, chunks;      // chunk: sorted positions a CTA, a multiple of kRedWarps
+  int fill;                      // dense: CTAs that write the rows no id names
   float scale;
   float* out;                    // dense: [n_rows][width]; sparse: [..][width]
   void* uniq;                    // sparse: row ids in ascending order
   int* n_uniq;
-  const int* heads;              // sparse: heads per chunk
+  const int* heads;              // sparse: heads per chunk (null: counted from the keys)
   // runs that cross a chunk's ends, joined by emb_join_kernel
   float *first, *tail;           // [chunks][width]
   int* state;                    // bit 0: a run goes on past the chunk, bit 1: the chunk is all one older run
@@ -440,212 +403,268 @@ struct ReduceArgs {
 };
 enum { kRunGoesOn = 1, kRunThrough = 2 };
 
+// The first position in the sorted keys with a key >= v, by a warp: 32 probes a
+// round.
+__device__ inline long long emb_lower_bound(const uint32_t* __restrict__ keys, long long R, uint32_t v) {
+  const int lane = threadIdx.x & 31;
+  long long lo = 0, hi = R;              // keys[lo - 1] < v <= keys[hi]
+  while (hi - lo > 0) {
+    const long long step = (hi - lo + 31) >> 5;
+    const long long at = min(hi - 1, lo + step * (lane + 1) - 1);
+    const unsigned less = __ballot_sync(~0u, keys[at] < v);   // a prefix of the lanes
+    const int n = __popc(less);
+    if (n == 32) return hi;
+    hi = min(hi - 1, lo + step * (n + 1) - 1);
+    lo = min(hi, lo + step * n);
+  }
+  return lo;
+}
+
+// Zeros for the 256 table rows from v0 that no id names.
+template <int CPL>
+__device__ inline void emb_fill_absent(const ReduceArgs& a, long long v0, int col) {
+  __shared__ unsigned s_there[kRedWarps];
+  __shared__ long long s_span[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < kRedWarps) s_there[threadIdx.x] = 0;
+  if (warp < 2) {
+    const long long p = emb_lower_bound(a.keys, a.R, (uint32_t)min((long long)a.n_rows, v0 + warp * 256));
+    if (lane == 0) s_span[warp] = p;
+  }
+  __syncthreads();
+  // the ids between: each position that begins a run marks its row
+  for (long long p = s_span[0] + threadIdx.x; p < s_span[1]; p += 32 * kRedWarps) {
+    const uint32_t k = a.keys[p];
+    if (p == s_span[0] || a.keys[p - 1] != k) atomicOr(&s_there[(k - v0) >> 5], 1u << ((k - v0) & 31));
+  }
+  __syncthreads();
+  if (col >= a.width) return;
+  float z[CPL];
+#pragma unroll
+  for (int e = 0; e < CPL; ++e) z[e] = 0.f;
+  const int n = (int)min(256LL, (long long)a.n_rows - v0);
+  for (int i = warp; i < n; i += kRedWarps)
+    if (!(s_there[i >> 5] >> (i & 31) & 1)) emb_st<CPL>(a.out + (v0 + i) * a.width + col, z);
+}
+
 // Sums the sorted rows of one chunk, run by run.  Warp w walks the positions
-// [w, w + 1) * chunk / 8 of the chunk, kRedBatch gathered rows in flight, a
+// [w, w + 1) * chunk / 8 of the chunk, a batch of gathered rows in flight, a
 // lane holding CPL columns (blockIdx.y picks 32 * CPL of them).  A run inside
 // a warp's positions is written at once; parts of runs that cross the warps'
 // borders are joined in shared memory, in position order, and parts that
-// cross the chunk's borders go to first / tail.  Dense: CTAs past the chunks
-// write zeros to the table rows that no id names, found by binary search in
-// the sorted ids, so every element of the table is written exactly once.
+// cross the chunk's borders go to first / tail.  Dense: fill CTAs, spread
+// between the chunks' so that their searches overlap the sums, write zeros to
+// the table rows that no id names, so that every element of the table is
+// written exactly once.
 template <typename T, typename Id, int CPL, bool DENSE>
 __global__ void __launch_bounds__(32 * kRedWarps) emb_reduce_kernel(const T* __restrict__ dout, ReduceArgs a) {
-  __shared__ float s_first[kRedWarps][32 * CPL], s_last[kRedWarps][32 * CPL];
-  __shared__ int s_flags[kRedWarps], s_heads[kRedWarps], s_before;
+  constexpr int BATCH = CPL <= 2 ? 16 : 8;   // 32 values a lane in flight
+  __shared__ __align__(16) float s_first[kRedWarps][32 * CPL], s_last[kRedWarps][32 * CPL];
+  __shared__ int s_flags[kRedWarps], s_heads[kRedWarps], s_part[kRedWarps];
   __shared__ long long s_row[kRedWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.y * 32 * CPL + lane * CPL;
   grid_dep_wait();
   grid_dep_launch();
-
-  if (DENSE && (int)blockIdx.x >= a.chunks) {
-    // 256 table rows a CTA: a row is absent when the first sorted key >= it is another
-    __shared__ unsigned s_absent[kRedWarps];
-    const long long v0 = (long long)(blockIdx.x - a.chunks) * 256;
-    const long long v = v0 + threadIdx.x;
-    bool absent = false;
-    if (v < a.n_rows) {
-      long long lo = 0, hi = a.R;
-      while (lo < hi) {
-        const long long mid = (lo + hi) >> 1;
-        if (a.keys[mid] < (uint32_t)v) lo = mid + 1; else hi = mid;
-      }
-      absent = lo == a.R || a.keys[lo] != (uint32_t)v;
+  int cta = blockIdx.x;
+  if (DENSE && a.fill) {
+    const long long all = (long long)a.chunks + a.fill;
+    const int f0 = (int)(cta * (long long)a.fill / all), f1 = (int)((cta + 1LL) * a.fill / all);
+    if (f1 > f0) {
+      emb_fill_absent<CPL>(a, f0 * 256LL, col);
+      return;
     }
-    const unsigned m = __ballot_sync(~0u, absent);
-    if (lane == 0) s_absent[warp] = m;
-    __syncthreads();
-    if (col >= a.width) return;
-    float z[CPL];
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) z[e] = 0.f;
-    for (int i = warp; i < 256; i += kRedWarps)
-      if (s_absent[i >> 5] >> (i & 31) & 1) emb_st<CPL>(a.out + (v0 + i) * a.width + col, z);
-    return;
+    cta -= f0;
   }
 
-  const int wrows = a.chunk / kRedWarps;   // a multiple of 32
-  const long long c0 = (long long)blockIdx.x * a.chunk;
+  const int wrows = a.chunk / kRedWarps;
+  const long long c0 = (long long)cta * a.chunk;
   const long long p0 = c0 + (long long)warp * wrows, p1 = min(a.R, p0 + wrows);
+  const bool on = col < a.width, some = p0 < p1;
 
-  long long urow = 0;   // sparse: output row of the next run that begins here
+  // the first 32 positions and the keys on either side of the warp's
+  uint32_t k = a.n_rows, r = 0;
+  if (p0 + lane < p1) {
+    k = a.keys[p0 + lane];
+    r = a.vals[p0 + lane];
+  }
+  const uint32_t prev = some && p0 > 0 ? a.keys[p0 - 1] : a.n_rows;
+  const uint32_t next = some && p1 < a.R ? a.keys[p1] : a.n_rows;
+  const uint32_t last = some ? a.keys[p1 - 1] : a.n_rows;
+
+  // sparse: heads in the chunks before (all of them at CTA 0, for the count)
+  int part = 0;
+  const bool count_all = !DENSE && cta == 0 && blockIdx.y == 0;
   if (!DENSE) {
-    int n = 0;
-    for (long long p = p0 + lane; p < p1; p += 32) {
-      const uint32_t k = a.keys[p];
-      n += k < a.n_rows && (p == 0 || a.keys[p - 1] != k);
-    }
-    n = __reduce_add_sync(~0u, n);
-    int before = 0, all = 0;
-    const bool count_all = blockIdx.x == 0 && blockIdx.y == 0;
-    for (int i = threadIdx.x; i < (count_all ? a.chunks : (int)blockIdx.x); i += 32 * kRedWarps) {
-      const int h = a.heads[i];
-      all += h;
-      if (i < (int)blockIdx.x) before += h;
-    }
-    before = __reduce_add_sync(~0u, count_all ? all : before);
-    if (threadIdx.x == 0) s_before = 0;
-    __syncthreads();
-    if (lane == 0) {
-      s_heads[warp] = n;
-      if (before) atomicAdd(&s_before, before);   // integers: any order
-    }
-    __syncthreads();
-    if (count_all) {
-      if (threadIdx.x == 0) *a.n_uniq = s_before;
+    if (a.heads) {
+      for (int i = threadIdx.x; i < (count_all ? a.chunks : cta); i += 32 * kRedWarps) part += a.heads[i];
     } else {
-      urow = s_before;
+      for (long long p = threadIdx.x; p < (count_all ? a.R : c0); p += 32 * kRedWarps) {
+        const uint32_t q = a.keys[p];
+        part += q < a.n_rows && (p == 0 || a.keys[p - 1] != q);
+      }
     }
-    for (int w = 0; w < warp; ++w) urow += s_heads[w];
+  }
+
+  // which of the 32 positions begin a run, and how many are no padding
+  auto heads_of = [&](uint32_t before) {
+    uint32_t q = __shfl_up_sync(~0u, k, 1);
+    if (lane == 0) q = before;
+    return __ballot_sync(~0u, k < a.n_rows && k != q);
+  };
+  unsigned heads = heads_of(prev);
+  int n = __popc(__ballot_sync(~0u, k < a.n_rows));
+  float v[BATCH][CPL];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const uint32_t ri = __shfl_sync(~0u, r, (i0 + i) & 31);
+      if (i0 + i < n && on) emb_ld<CPL>(dout + (long long)ri * a.dout_ld + col, v[i]);
+    }
+  };
+  load(0);     // in flight over the count
+
+  const bool older = some && prev < a.n_rows && !(heads & 1) && n > 0;   // the first run began before
+  const bool goes_on = some && last < a.n_rows && next == last;          // the last one goes on after
+  Id* uniq = (Id*)a.uniq;
+  float* o = a.out + col;        // sparse: where the next run that begins here goes
+  long long urow = 0;
+  if (!DENSE) {
+    int mine = __popc(heads);
+    for (long long p = p0 + 32; p < p1; p += 32) {     // only with more than 32 positions a warp
+      const uint32_t q = p + lane < p1 ? a.keys[p + lane] : a.n_rows;
+      mine += __popc(__ballot_sync(~0u, q < a.n_rows && q != a.keys[p + lane - 1]));
+    }
+    part = __reduce_add_sync(~0u, part);
+    if (lane == 0) {
+      s_part[warp] = part;
+      s_heads[warp] = mine;
+    }
+    __syncthreads();
+    int before = lane < kRedWarps ? (count_all ? 0 : s_part[lane]) + (lane < warp ? s_heads[lane] : 0) : 0;
+    urow = __reduce_add_sync(~0u, before);
+    if (count_all && warp == 0) {
+      const int all = __reduce_add_sync(~0u, lane < kRedWarps ? s_part[lane] : 0);
+      if (lane == 0) *a.n_uniq = all;
+    }
+    o += urow * a.width;
   }
 
   float acc[CPL];
 #pragma unroll
   for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
-  uint32_t cur = a.n_rows;          // key of the open run, n_rows: none
-  long long cur_row = 0;
-  bool older = false;               // the open run began before this warp's positions
-  int flags = 0;                    // bit 0: an older run's part in s_first, bit 1: a run goes on after (s_last), bit 2: all one older run
-  const bool on = col < a.width;
-
-  auto flush = [&]() {              // the open run ends inside the warp's positions
-    if (cur >= a.n_rows) return;
-    if (older) {
+  // the open run's sum goes to dst: its output row, times the scale, or (part_of)
+  // shared memory, for a piece of a run that crosses the warp's border
+  float* dst = older ? &s_first[warp][lane * CPL] : nullptr;
+  bool part_of = older;
+  bool open = older, begun = false;      // begun: a run began here
+  long long row = 0;                     // output row of the run that began here last
+  auto flush = [&]() {
+    if (open && (on || part_of)) {       // lanes past the width own no output
+      float w[CPL];
 #pragma unroll
-      for (int e = 0; e < CPL; ++e) s_first[warp][lane * CPL + e] = acc[e];
-      flags |= 1;
-    } else if (on) {
+      for (int e = 0; e < CPL; ++e) w[e] = part_of ? acc[e] : acc[e] * a.scale;
 #pragma unroll
-      for (int e = 0; e < CPL; ++e) acc[e] *= a.scale;
-      emb_st<CPL>(a.out + cur_row * a.width + col, acc);
+      for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
+      emb_st<CPL>(dst, w);
     }
   };
 
-  for (long long p = p0; p < p1; p += 32) {
-    const int n = (int)min(32LL, p1 - p);
-    const uint32_t k = lane < n ? a.keys[p + lane] : a.n_rows;
-    const uint32_t r = lane < n ? a.vals[p + lane] : 0;
-    if (__shfl_sync(~0u, k, 0) >= a.n_rows) break;   // padding only from here on
-    if (p == p0 && p0 > 0) {
-      const uint32_t prev = a.keys[p0 - 1];
-      if (prev == __shfl_sync(~0u, k, 0)) {
-        cur = prev;
-        older = true;
-      }
+  for (long long p = p0; n > 0; ) {
+    if (!DENSE) {
+      if (blockIdx.y == 0 && (heads >> lane & 1)) uniq[urow + __popc(heads & ((1u << lane) - 1))] = (Id)k;
     }
-    for (int i0 = 0; i0 < n; i0 += kRedBatch) {
-      float v[kRedBatch][CPL];
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+      if (i0 > 0 || p > p0) load(i0);
 #pragma unroll
-      for (int i = 0; i < kRedBatch; ++i) {
-        const uint32_t ki = __shfl_sync(~0u, k, i0 + i), ri = __shfl_sync(~0u, r, i0 + i);
-        if (ki < a.n_rows && on) {
-          emb_ld<CPL>(dout + (long long)ri * a.dout_ld + col, v[i]);
-        } else {
+      for (int i = 0; i < BATCH; ++i) {
+        if (i0 + i < n) {                       // the same for the whole warp, as every branch here
+          if (heads >> (i0 + i) & 1) {
+            flush();
+            if (DENSE) {
+              row = __shfl_sync(~0u, k, i0 + i);
+              dst = a.out + row * a.width + col;
+            } else {
+              dst = o;
+              o += a.width;
+              row = urow++;
+            }
+            part_of = false;
+            open = begun = true;
+          }
+          if (on) {
 #pragma unroll
-          for (int e = 0; e < CPL; ++e) v[i][e] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kRedBatch; ++i) {
-        const uint32_t ki = __shfl_sync(~0u, k, i0 + i);
-        if (i0 + i < n && ki != cur) {    // the same for the whole warp
-          flush();
-          cur = ki;
-          older = false;
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
-          if (ki < a.n_rows) {
-            cur_row = DENSE ? (long long)ki : urow++;
-            if (!DENSE && blockIdx.y == 0 && lane == 0) ((Id*)a.uniq)[cur_row] = (Id)ki;
+            for (int e = 0; e < CPL; ++e) acc[e] += v[i][e];
           }
         }
-        if (i0 + i < n) {
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) acc[e] += v[i][e];
-        }
       }
     }
+    p += 32;
+    if (p >= p1 || n < 32) break;
+    const uint32_t before = __shfl_sync(~0u, k, 31);
+    k = p + lane < p1 ? a.keys[p + lane] : a.n_rows;
+    r = p + lane < p1 ? a.vals[p + lane] : 0;
+    heads = heads_of(before);
+    n = __popc(__ballot_sync(~0u, k < a.n_rows));
   }
-  const bool goes_on = cur < a.n_rows && p1 < a.R && p0 < p1 && a.keys[p1] == cur;
   if (goes_on) {
-    if (older) {
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) s_first[warp][lane * CPL + e] = acc[e];
-      flags |= 1 | 4;
-    } else {
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) s_last[warp][lane * CPL + e] = acc[e];
-      flags |= 2;
-    }
-  } else {
-    flush();
+    dst = begun ? &s_last[warp][lane * CPL] : &s_first[warp][lane * CPL];
+    part_of = true;
   }
+  flush();
   if (lane == 0) {
-    s_flags[warp] = flags;
-    s_row[warp] = cur_row;
+    // bit 0: an older run's part in s_first, bit 1: a run goes on after
+    // (s_last), bit 2: all one older run
+    s_flags[warp] = (older ? 1 : 0) | (goes_on && begun ? 2 : 0) | (goes_on && !begun ? 4 : 0);
+    s_row[warp] = row;
   }
   __syncthreads();
   if (warp) return;
 
   // warp 0 joins the warps' parts in order
+  const int flags = lane < kRedWarps ? s_flags[lane] : 0;
+  if (!__any_sync(~0u, flags)) {         // no run crosses a border
+    if (a.chunks > 1 && lane == 0 && blockIdx.y == 0) a.state[cta] = 0;
+    return;
+  }
   float head[CPL], carry[CPL];
 #pragma unroll
   for (int e = 0; e < CPL; ++e) head[e] = carry[e] = 0.f;
-  bool open = false, through = true;   // an open run that began in this chunk; the chunk so far is one older run
-  long long row = 0;
+  bool open_run = false, through = true;   // an open run that began in this chunk; the chunk so far is one older run
+  long long at = 0;
   for (int w = 0; w < kRedWarps; ++w) {
-    const int f = s_flags[w];
+    const int f = __shfl_sync(~0u, flags, w);
     if (f & 1) {
 #pragma unroll
       for (int e = 0; e < CPL; ++e) {
         const float x = s_first[w][lane * CPL + e];
-        if (open) carry[e] += x; else head[e] += x;
+        if (open_run) carry[e] += x; else head[e] += x;
       }
-      if (!(f & 4) && open) {
+      if (!(f & 4) && open_run) {
         if (on) {
 #pragma unroll
           for (int e = 0; e < CPL; ++e) carry[e] *= a.scale;
-          emb_st<CPL>(a.out + row * a.width + col, carry);
+          emb_st<CPL>(a.out + at * a.width + col, carry);
         }
-        open = false;
+        open_run = false;
       }
     }
     if (!(f & 4)) through = false;
     if (f & 2) {
 #pragma unroll
       for (int e = 0; e < CPL; ++e) carry[e] = s_last[w][lane * CPL + e];
-      open = true;
-      row = s_row[w];
+      open_run = true;
+      at = s_row[w];
     }
   }
   if (a.chunks > 1) {
     if (on) {
-      emb_st<CPL>(a.first + (long long)blockIdx.x * a.width + col, head);
-      if (open) emb_st<CPL>(a.tail + (long long)blockIdx.x * a.width + col, carry);
+      emb_st<CPL>(a.first + (long long)cta * a.width + col, head);
+      if (open_run) emb_st<CPL>(a.tail + (long long)cta * a.width + col, carry);
     }
     if (lane == 0 && blockIdx.y == 0) {
-      a.state[blockIdx.x] = (open ? kRunGoesOn : 0) | (through ? kRunThrough : 0);
-      a.tail_row[blockIdx.x] = row;
+      a.state[cta] = (open_run ? kRunGoesOn : 0) | (through ? kRunThrough : 0);
+      a.tail_row[cta] = at;
     }
   }
 }
@@ -654,8 +673,8 @@ __global__ void __launch_bounds__(32 * kRedWarps) emb_reduce_kernel(const T* __r
 // and its part of the chunk it ends in, added by warps over strided chunks
 // and then in warp order (a fixed order).
 template <int CPL>
-__global__ void __launch_bounds__(1024) emb_join_kernel(ReduceArgs a) {
-  __shared__ float part[32][32 * CPL];
+__global__ void __launch_bounds__(32 * kJoinWarps) emb_join_kernel(ReduceArgs a) {
+  __shared__ float part[kJoinWarps][32 * CPL];
   __shared__ int s_end;
   grid_dep_wait();
   grid_dep_launch();
@@ -685,7 +704,7 @@ __global__ void __launch_bounds__(1024) emb_join_kernel(ReduceArgs a) {
   for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
   if (on) {
 #pragma unroll 4
-    for (int i = c + 1 + warp; i <= end; i += 32) {
+    for (int i = c + 1 + warp; i <= end; i += kJoinWarps) {
       float v[CPL];
       emb_ld<CPL>(a.first + (long long)i * a.width + col, v);
 #pragma unroll
@@ -698,7 +717,7 @@ __global__ void __launch_bounds__(1024) emb_join_kernel(ReduceArgs a) {
   if (warp || !on) return;
   float s[CPL];
   emb_ld<CPL>(a.tail + (long long)c * a.width + col, s);
-  for (int w = 0; w < min(32, end - c); ++w)
+  for (int w = 0; w < min(kJoinWarps, end - c); ++w)
 #pragma unroll
     for (int e = 0; e < CPL; ++e) s[e] += part[w][lane * CPL + e];
 #pragma unroll

@@ -20,25 +20,23 @@ static bool mode_ok(int32_t mode) { return mode == ONETRANS_BF16 || mode == ONET
 template <typename Tt, typename To, typename Id>
 static onetrans_status lookup_impl(const void* table, long long n_rows, int width, const void* ids, long long R,
                                    float scale, void* out, long long out_ld, cudaStream_t st) {
-  // 16 bytes of the wider type's row per access where the rows keep that alignment
+  // 16 bytes of the narrower type's row per access where the rows keep that alignment
   int ve = sizeof(Tt) == 4 && sizeof(To) == 4 ? 4 : 8;
   while (width % ve || out_ld % ve) ve >>= 1;
-  const int cpr = width / ve;
-  // about a thousand groups of columns a CTA, fewer when that leaves SMs idle
-  const long long per = std::min<long long>(kLookThreads * kLookUnroll,
-                                            std::max<long long>(kLookThreads, R * cpr / device_sm_count()));
-  const int rows = (int)std::max<long long>(1, per / cpr);
-  const dim3 grid((unsigned)cdiv(R, rows));
+  const int groups = width / ve, cpr = std::min(groups, kLookThreads), rpb = kLookThreads / cpr;
+  // eight rows in flight per thread once that still gives every SM two CTAs
+  const bool many = R >= 2LL * 148 * 8 * rpb;
+  const dim3 grid((unsigned)cdiv(R, rpb * (many ? 8 : 1)), (unsigned)cdiv(groups, cpr));
   ProfScope prof(PK_EMBEDDING, 0.0, (double)R * (sizeof(Id) + width * (double)(sizeof(Tt) + sizeof(To))), st);
-  auto go = [&](auto kernel) {
-    launch_dependent(kernel, grid, dim3(kLookThreads), 0, st, (const Tt*)table, (uint32_t)n_rows, width,
-                     (const Id*)ids, R, rows, scale, (To*)out, out_ld);
+  auto go = [&](auto one, auto eight) {
+    launch_dependent(many ? eight : one, grid, dim3(kLookThreads), 0, st, (const Tt*)table, (uint32_t)n_rows, width,
+                     (const Id*)ids, R, cpr, scale, (To*)out, out_ld);
   };
   switch (ve) {
-    case 8: go(emb_lookup_kernel<Tt, To, Id, 8>); break;
-    case 4: go(emb_lookup_kernel<Tt, To, Id, 4>); break;
-    case 2: go(emb_lookup_kernel<Tt, To, Id, 2>); break;
-    default: go(emb_lookup_kernel<Tt, To, Id, 1>); break;
+    case 8: go(emb_lookup_kernel<Tt, To, Id, 8, 1>, emb_lookup_kernel<Tt, To, Id, 8, 8>); break;
+    case 4: go(emb_lookup_kernel<Tt, To, Id, 4, 1>, emb_lookup_kernel<Tt, To, Id, 4, 8>); break;
+    case 2: go(emb_lookup_kernel<Tt, To, Id, 2, 1>, emb_lookup_kernel<Tt, To, Id, 2, 8>); break;
+    default: go(emb_lookup_kernel<Tt, To, Id, 1, 1>, emb_lookup_kernel<Tt, To, Id, 1, 8>); break;
   }
   return last_launch();
 }
@@ -66,19 +64,19 @@ static int key_bits(long long n_rows) {
 
 // Tiles whose counts every CTA of a pass adds up itself; with more, a scan
 // kernel turns them into prefixes first (each CTA reads tiles x digits counts).
-static const int kSortDirectTiles = 64;
+static const int kSortDirectTiles = 128;
 
 template <typename T, typename Id, bool DENSE>
 static onetrans_status emb_reduce_launch(const EmbGrad& g, ReduceArgs a, cudaStream_t st) {
   int cpl = 1;
   while (cpl < 8 && 32 * cpl < g.width) cpl *= 2;
   while (g.width % cpl || g.dout_ld % cpl) cpl >>= 1;
-  const unsigned fill = DENSE ? (unsigned)cdiv(g.n_rows, 256) : 0u;
-  const dim3 grid((unsigned)a.chunks + fill, (unsigned)cdiv(g.width, 32 * cpl));
+  a.fill = DENSE ? (int)cdiv(g.n_rows, 256) : 0;
+  const dim3 grid((unsigned)(a.chunks + a.fill), (unsigned)cdiv(g.width, 32 * cpl));
   const dim3 jgrid((unsigned)a.chunks, grid.y);
   auto go = [&](auto reduce, auto join) {
     launch_dependent(reduce, grid, dim3(32 * kRedWarps), 0, st, (const T*)g.dout, a);
-    if (a.chunks > 1) launch_dependent(join, jgrid, dim3(1024), 0, st, a);
+    if (a.chunks > 1) launch_dependent(join, jgrid, dim3(32 * kJoinWarps), 0, st, a);
   };
   switch (cpl) {
     case 8: go(emb_reduce_kernel<T, Id, 8, DENSE>, emb_join_kernel<8>); break;
@@ -93,8 +91,10 @@ template <typename Id>
 static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes, cudaStream_t st, size_t* need) {
   const long long R = g.R;
   const int tiles = (int)cdiv(R, kSortTile);
-  // chunks of sorted positions, 4096 chunks at most up to R = 2^20
-  const int chunk = 32 * kRedWarps * (int)cdiv(std::max<long long>(R, 1), 1 << 20);
+  // sorted positions a warp: few while that leaves all of them resident at once
+  // (4 CTAs an SM), at most 4096 chunks up to 2^20 positions
+  const int wrows = R <= 148 * 4 * 8 * kRedWarps ? 8 : R <= 148 * 4 * 16 * kRedWarps ? 16 : 32 * (int)cdiv(R, 1 << 20);
+  const int chunk = kRedWarps * wrows;
   const int chunks = (int)cdiv(R, chunk);
   Carve cv(ws, ws_bytes);
   uint32_t* keys[2];
@@ -125,11 +125,10 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
                  row_bytes + (double)R * sizeof(Id) +
                      (double)(dense ? g.n_rows : std::min(R, g.n_rows)) * g.width * 4, st);
   int at = 0;   // the sorted pairs are in keys[at], vals[at]
-  if (R > 0 && tiles == 1) {
-    const size_t smem = (size_t)kSortWarps * bins * 2 + std::max(bins, 32) * 4 + 2 * kSortTile * 4;
-    if (!allow_smem(sort_small_kernel<Id>, smem)) return ONETRANS_ERR_CUDA;
-    launch_dependent(sort_small_kernel<Id>, dim3(1), dim3(kSortThreads), smem, st, (const Id*)g.ids, n_rows, (int)R,
-                     passes, per, keys[0], vals[0], dense ? (int*)nullptr : heads, chunk);
+  const bool ranked = R <= kRankMax;
+  if (R > 0 && ranked) {
+    launch_dependent(sort_rank_kernel<Id>, dim3((unsigned)cdiv(R, kRankThreads / 32 * kRankIds)), dim3(kRankThreads), 0,
+                     st, (const Id*)g.ids, n_rows, (int)R, keys[0], vals[0]);
   } else if (R > 0) {
     const long long per_pass = (long long)tiles * bins;
     SortArgs a;
@@ -151,7 +150,7 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
       a.shift = p * per;
       a.hist = hist + per_pass * p;
       a.hist_next = p + 1 < passes ? a.hist + per_pass : nullptr;
-      if (a.scanned) launch_dependent(sort_scan_kernel, dim3((unsigned)cdiv(bins, 32)), dim3(kSortThreads), 0, st, a);
+      if (a.scanned) launch_dependent(sort_scan_kernel, dim3((unsigned)cdiv(bins, 32)), dim3(1024), 0, st, a);
       const uint32_t *ki = keys[at], *vi = vals[at];
       if (p > 0) at ^= 1;
       if (p == 0)
@@ -174,7 +173,7 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
   r.width = g.width; r.chunk = chunk; r.chunks = chunks;
   r.scale = g.scale;
   r.out = g.out; r.uniq = g.uniq; r.n_uniq = g.n_uniq;
-  r.heads = heads; r.first = first; r.tail = tail; r.state = state; r.tail_row = tail_row;
+  r.heads = ranked ? nullptr : heads; r.first = first; r.tail = tail; r.state = state; r.tail_row = tail_row;
   if (g.dout_mode == ONETRANS_BF16)
     return dense ? emb_reduce_launch<__nv_bfloat16, int32_t, true>(g, r, st)
                  : emb_reduce_launch<__nv_bfloat16, Id, false>(g, r, st);
@@ -616,6 +615,9 @@ onetrans_status onetrans_tokenize_routed(const onetrans_model* m, const void* ev
     return ONETRANS_ERR_INVALID_ARG;
   const PlanBuf p = plan_buf(m, const_cast<void*>(plan), R, k);
   if (p.bytes > plan_bytes) return ONETRANS_ERR_CAPACITY;
+  size_t need = 0;
+  OT_TRY(tokenize_routed_any(m, nullptr, R, k, nullptr, 0, nullptr, &need));
+  if (ws_bytes < need) return ONETRANS_ERR_CAPACITY;
   RoutedCall c;
   std::memset(&c, 0, sizeof(c));
   c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
@@ -662,6 +664,9 @@ onetrans_status onetrans_tokenize_routed_backward(const onetrans_model* m, const
     return ONETRANS_ERR_INVALID_ARG;
   const PlanBuf p = plan_buf(m, const_cast<void*>(plan), R, k);
   if (p.bytes > plan_bytes) return ONETRANS_ERR_CAPACITY;
+  size_t need = 0;
+  OT_TRY(routed_backward_any(m, nullptr, R, k, nullptr, 0, nullptr, &need));
+  if (ws_bytes < need) return ONETRANS_ERR_CAPACITY;
   c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
   c.dtokens = dtokens; c.dtokens_mode = dtokens_mode;
   c.rows = TokenRows{(int)rows_per_sample, sample_ld};
