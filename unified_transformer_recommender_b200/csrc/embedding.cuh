@@ -122,20 +122,25 @@ __global__ void __launch_bounds__(kLookThreads) emb_lookup_kernel(const Tt* __re
 }
 
 // ------------------------------------------------------------------- sort --
-// Stable least-significant-digit radix sort of (key, position).  A tile of
-// kSortTile items per CTA; a pass ranks the items of its tile per digit (per
-// warp by matching lanes, then across warps) and scatters them behind the
-// same digits of the tiles before.  The counts of every (tile, digit) of a
-// pass are ready when it starts: the first pass's come from sort_hist_kernel,
-// a later pass's are added up, as integers, by the pass before it while it
-// scatters (a destination's tile is known there).
-constexpr int kSortThreads = 512, kSortItems = 4, kSortTile = kSortThreads * kSortItems;
-constexpr int kSortWarps = kSortThreads / 32, kSortMaxBits = 8;
+// Stable least-significant-digit radix sort of (key, position).  A CTA takes a
+// tile of 512 x ITEMS items; a pass ranks the items of its tile per digit (per
+// warp by ballots, then across warps), puts the tile in order in shared memory
+// and writes it out behind the same digits of the tiles before, so that
+// neighbouring threads mostly write neighbouring places.  The counts of every
+// (tile, digit) of a pass are ready when it starts: the first pass's come from
+// sort_hist_kernel, a later pass's are added up, as integers, by the pass
+// before it while it writes (a destination's tile is known there).
+//
+// A pass is a chain of latencies more than work.  Measured on 75392 ids of 20
+// bits (three passes of 7): tiles of 1024 items 74 CTAs, of 4096 items 19 CTAs;
+// the fewer items a CTA ranks the sooner it is done, until adding up the
+// counts of all tiles costs more.
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kSortMinBits = 4, kSortMaxBits = 8;
 
 struct SortArgs {
   uint32_t n_rows;       // keys 0 .. n_rows
   long long R;
-  int tiles, bits, shift;   // digit = (key >> shift) & (2^bits - 1)
+  int tile, tiles, bits, shift;   // items a tile; digit = (key >> shift) & (2^bits - 1)
   int scanned;           // hist already holds the tile prefixes, tot the digit totals
   int* hist;             // this pass: [tiles][2^bits]
   int* tot;              // [2^bits]
@@ -143,28 +148,26 @@ struct SortArgs {
 };
 
 // Exclusive prefix of v over the CTA's threads; every thread calls it.
-__device__ inline int block_exclusive(int v, int* warp_sums, int& total) {
+__device__ inline unsigned long long block_exclusive(unsigned long long v, unsigned long long* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int x = v;
+  unsigned long long x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, x, o);
+    const unsigned long long y = __shfl_up_sync(~0u, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();   // warp_sums free again
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int s = lane < nw ? warp_sums[lane] : 0;
+    unsigned long long s = lane < nw ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(~0u, s, o);
+      const unsigned long long y = __shfl_up_sync(~0u, s, o);
       if (lane >= o) s += y;
     }
     warp_sums[lane] = s;
   }
   __syncthreads();
-  total = warp_sums[31];
   return x - v + (warp ? warp_sums[warp - 1] : 0);
 }
 
@@ -177,10 +180,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const Id* __res
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
-  const long long i0 = (long long)blockIdx.x * kSortTile;
-#pragma unroll
-  for (int u = 0; u < kSortItems; ++u) {
-    const long long i = i0 + u * kSortThreads + threadIdx.x;
+  const long long i0 = (long long)blockIdx.x * a.tile;
+  for (int u = 0; u < a.tile; u += kSortThreads) {
+    const long long i = i0 + u + threadIdx.x;
     if (i < a.R) atomicAdd(&h[(emb_key(ids[i], a.n_rows) >> a.shift) & (bins - 1)], 1);
   }
   __syncthreads();
@@ -229,92 +231,134 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(SortArgs a) {
 // zeroed by the caller; on return wh[w][b] is the count of digit b in the
 // warps before w.  rank[u]: the item's rank among its warp's items of that
 // digit.  Warp w's items are contiguous, item u of lane l at
-// (w * kSortItems + u) * 32 + l.
-__device__ inline void sort_rank(const uint32_t* digit, const bool* on, uint16_t* wh, int bins, int* rank) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint16_t* mine = wh + (long long)warp * bins;
+// (w * ITEMS + u) * 32 + l.
+template <int ITEMS>
+__device__ inline void sort_rank(const uint32_t* digit, const bool* on, uint16_t* wh, int bits, int* rank) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
+  uint16_t* mine = wh + warp * bins;
+  unsigned same[ITEMS];
 #pragma unroll
-  for (int u = 0; u < kSortItems; ++u) {
-    const uint32_t same = __match_any_sync(~0u, on[u] ? digit[u] : 0xffffffffu);
-    const int below = __popc(same & ((1u << lane) - 1));
+  for (int u = 0; u < ITEMS; ++u) {   // the lanes with this digit: one ballot per bit
+    same[u] = __ballot_sync(~0u, on[u]);
+#pragma unroll
+    for (int i = 0; i < kSortMaxBits; ++i)
+      if (i < bits) {
+        const bool one = digit[u] >> i & 1;
+        const unsigned v = __ballot_sync(~0u, one);
+        same[u] &= one ? v : ~v;
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const int below = __popc(same[u] & ((1u << lane) - 1));
     int base = 0;
     if (on[u]) base = mine[digit[u]];
     __syncwarp();
-    if (on[u] && below == 0) mine[digit[u]] = (uint16_t)(base + __popc(same));
+    if (on[u] && below == 0) mine[digit[u]] = (uint16_t)(base + __popc(same[u]));
     __syncwarp();
     rank[u] = base + below;
   }
   __syncthreads();
   for (int b = threadIdx.x; b < bins; b += kSortThreads) {
-    int s = 0;
-#pragma unroll 8
+    int c[kSortWarps], s = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) c[w] = wh[w * bins + b];
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const int c = wh[w * bins + b];
       wh[w * bins + b] = (uint16_t)s;
-      s += c;
+      s += c[w];
     }
   }
   __syncthreads();
 }
 
 // One pass.  FIRST: items are (id, position) from the caller's ids.
-template <typename Id, bool FIRST>
+template <typename Id, bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const Id* __restrict__ ids,
                                                                  const uint32_t* __restrict__ keys_in,
                                                                  const uint32_t* __restrict__ vals_in,
                                                                  uint32_t* __restrict__ keys, uint32_t* __restrict__ vals,
                                                                  SortArgs a, int next_bits, int next_shift) {
-  extern __shared__ uint16_t sort_sm[];   // [kSortWarps][bins] u16, then [bins] int digit bases
-  __shared__ int warp_sums[32];
+  constexpr int TILE = kSortThreads * ITEMS;
+  extern __shared__ __align__(16) uint8_t sort_sm[];
+  __shared__ unsigned long long warp_sums[32];
   const int bins = 1 << a.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int* base = (int*)(sort_sm + kSortWarps * bins);
-  for (int i = threadIdx.x; i < kSortWarps * bins / 2; i += kSortThreads) ((uint32_t*)sort_sm)[i] = 0;
+  uint2* pairs = (uint2*)sort_sm;                       // [TILE] the tile in digit order
+  int2* base = (int2*)(pairs + TILE);              // [bins] x: place of the digit's first item minus y, y: its first slot in the tile
+  uint16_t* wh = (uint16_t*)(base + bins);              // [kSortWarps][bins]
+  for (int i = threadIdx.x; i < kSortWarps * bins / 2; i += kSortThreads) ((uint32_t*)wh)[i] = 0;
   grid_dep_wait();
   grid_dep_launch();
-  uint32_t key[kSortItems], val[kSortItems], digit[kSortItems];
-  bool on[kSortItems];
+  const long long i0 = (long long)blockIdx.x * TILE;
+  const int n = (int)min((long long)TILE, a.R - i0);
+  uint32_t key[ITEMS], val[ITEMS], digit[ITEMS];
+  bool on[ITEMS];
 #pragma unroll
-  for (int u = 0; u < kSortItems; ++u) {
-    const long long i = (long long)blockIdx.x * kSortTile + (warp * kSortItems + u) * 32 + lane;
-    on[u] = i < a.R;
-    key[u] = !on[u] ? 0u : FIRST ? emb_key(ids[i], a.n_rows) : keys_in[i];
-    val[u] = !on[u] ? 0u : FIRST ? (uint32_t)i : vals_in[i];
-    digit[u] = (key[u] >> a.shift) & (bins - 1);
+  for (int u = 0; u < ITEMS; ++u) {
+    const int j = (warp * ITEMS + u) * 32 + lane;
+    on[u] = j < n;
+    key[u] = !on[u] ? 0u : FIRST ? emb_key(ids[i0 + j], a.n_rows) : keys_in[i0 + j];
+    val[u] = !on[u] ? 0u : FIRST ? (uint32_t)(i0 + j) : vals_in[i0 + j];
   }
-  // where the tile's items of each digit begin: two threads a digit (the
-  // even and the odd tiles), neighbouring lanes
-  static_assert(kSortThreads == 2 << kSortMaxBits, "two threads per digit");
-  const int b = threadIdx.x >> 1, odd = threadIdx.x & 1;
-  int tot = 0, mine = 0;
-  if (b < bins) {
-    if (a.scanned) {
-      if (!odd) {
-        tot = a.tot[b];
-        mine = a.hist[(long long)blockIdx.x * bins + b];
-      }
-    } else {
-#pragma unroll 8
-      for (int t = odd; t < a.tiles; t += 2) {
-        const int c = a.hist[(long long)t * bins + b];
-        tot += c;
-        if (t < (int)blockIdx.x) mine += c;
+  // where the tile's items of each digit begin, in the whole and in the tile:
+  // neighbouring threads share a digit and its tiles' counts, 16 in flight each
+  static_assert(kSortThreads >= 2 << kSortMaxBits && kSortThreads >> kSortMinBits <= 32, "2 to 32 threads per digit");
+  const int tpd = kSortThreads >> a.bits, b = threadIdx.x / tpd, sub = threadIdx.x & (tpd - 1);
+  int tot = 0, before = 0, own = 0;
+  if (a.scanned) {
+    if (sub == 0) {
+      tot = a.tot[b];
+      before = a.hist[(long long)blockIdx.x * bins + b];
+      own = (blockIdx.x + 1 < gridDim.x ? a.hist[(long long)(blockIdx.x + 1) * bins + b] : tot) - before;
+    }
+  } else {
+    for (int t0 = sub; t0 < a.tiles; t0 += 16 * tpd) {
+      int c[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) c[i] = t0 + tpd * i < a.tiles ? a.hist[(long long)(t0 + tpd * i) * bins + b] : 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        tot += c[i];
+        if (t0 + tpd * i < (int)blockIdx.x) before += c[i];
+        if (t0 + tpd * i == (int)blockIdx.x) own += c[i];
       }
     }
   }
-  mine += __shfl_xor_sync(~0u, mine, 1);
-  int all;
-  const int ex = block_exclusive(tot, warp_sums, all);   // at the even thread: the digits before
-  if (b < bins && !odd) base[b] = ex + mine;
-  int rank[kSortItems];
-  sort_rank(digit, on, sort_sm, bins, rank);
 #pragma unroll
-  for (int u = 0; u < kSortItems; ++u) {
-    if (!on[u]) continue;
-    const int to = base[digit[u]] + sort_sm[warp * bins + digit[u]] + rank[u];
-    keys[to] = key[u];
-    vals[to] = val[u];
-    if (a.hist_next)
-      atomicAdd(&a.hist_next[((long long)(to / kSortTile) << next_bits) + ((key[u] >> next_shift) & ((1 << next_bits) - 1))], 1);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_xor_sync(~0u, before, o);
+    if (o < tpd) before += x;
+  }
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) digit[u] = (key[u] >> a.shift) & (bins - 1);
+  const unsigned long long ex = block_exclusive((unsigned long long)(unsigned)tot | (unsigned long long)own << 32, warp_sums);
+  if (sub == 0) {
+    const int slot = (int)(ex >> 32);
+    base[b] = make_int2((int)(unsigned)ex + before - slot, slot);
+  }
+  int rank[ITEMS];
+  sort_rank<ITEMS>(digit, on, wh, a.bits, rank);
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u)
+    if (on[u]) pairs[base[digit[u]].y + wh[warp * bins + digit[u]] + rank[u]] = make_uint2(key[u], val[u]);
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const int j = u * kSortThreads + threadIdx.x;
+    int counter = -1;
+    if (j < n) {
+      const uint2 q = pairs[j];
+      const int to = base[(q.x >> a.shift) & (bins - 1)].x + j;
+      keys[to] = q.x;
+      vals[to] = q.y;
+      counter = ((to / TILE) << next_bits) + ((q.x >> next_shift) & ((1 << next_bits) - 1));
+    }
+    // a popular id sends many lanes to one counter: one add for all of them
+    // (adds to the same address queue up)
+    if (a.hist_next) {
+      const unsigned same = __match_any_sync(~0u, counter);
+      if (counter >= 0 && (same & ((1u << lane) - 1)) == 0) atomicAdd(&a.hist_next[counter], __popc(same));
+    }
   }
 }
 
@@ -457,8 +501,8 @@ __device__ inline void emb_fill_absent(const ReduceArgs& a, long long v0, int co
 // the table rows that no id names, so that every element of the table is
 // written exactly once.
 template <typename T, typename Id, int CPL, bool DENSE>
-__global__ void __launch_bounds__(32 * kRedWarps) emb_reduce_kernel(const T* __restrict__ dout, ReduceArgs a) {
-  constexpr int BATCH = CPL <= 2 ? 16 : 8;   // 32 values a lane in flight
+__global__ void __launch_bounds__(32 * kRedWarps, CPL <= 2 ? 4 : CPL == 4 ? 3 : 2) emb_reduce_kernel(const T* __restrict__ dout, ReduceArgs a) {
+  constexpr int BATCH = CPL == 1 ? 16 : 8;    // gathered rows in flight per warp
   __shared__ __align__(16) float s_first[kRedWarps][32 * CPL], s_last[kRedWarps][32 * CPL];
   __shared__ int s_flags[kRedWarps], s_heads[kRedWarps], s_part[kRedWarps];
   __shared__ long long s_row[kRedWarps];

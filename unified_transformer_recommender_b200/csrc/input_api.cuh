@@ -56,6 +56,9 @@ struct EmbGrad {
   int32_t* n_uniq;
 };
 
+// Sort items a thread: see the measurement at the sort kernels.
+static int sort_items(long long R) { return R <= 160 * 1024 ? 2 : R <= 320 * 1024 ? 4 : 8; }
+
 static int key_bits(long long n_rows) {
   int b = 1;
   while ((n_rows >> b) != 0) ++b;
@@ -64,7 +67,7 @@ static int key_bits(long long n_rows) {
 
 // Tiles whose counts every CTA of a pass adds up itself; with more, a scan
 // kernel turns them into prefixes first (each CTA reads tiles x digits counts).
-static const int kSortDirectTiles = 128;
+static const int kSortDirectTiles = 192;
 
 template <typename T, typename Id, bool DENSE>
 static onetrans_status emb_reduce_launch(const EmbGrad& g, ReduceArgs a, cudaStream_t st) {
@@ -90,10 +93,11 @@ static onetrans_status emb_reduce_launch(const EmbGrad& g, ReduceArgs a, cudaStr
 template <typename Id>
 static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes, cudaStream_t st, size_t* need) {
   const long long R = g.R;
-  const int tiles = (int)cdiv(R, kSortTile);
+  const int items = sort_items(R), tile = kSortThreads * items;
+  const int tiles = (int)cdiv(R, tile);
   // sorted positions a warp: few while that leaves all of them resident at once
   // (4 CTAs an SM), at most 4096 chunks up to 2^20 positions
-  const int wrows = R <= 148 * 4 * 8 * kRedWarps ? 8 : R <= 148 * 4 * 16 * kRedWarps ? 16 : 32 * (int)cdiv(R, 1 << 20);
+  const int wrows = R <= 148 * 4 * 8 * kRedWarps ? 8 : R <= 1 << 19 ? 16 : 32 * (int)cdiv(R, 1 << 20);
   const int chunk = kRedWarps * wrows;
   const int chunks = (int)cdiv(R, chunk);
   Carve cv(ws, ws_bytes);
@@ -119,7 +123,7 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
   const bool dense = !g.uniq;
   const uint32_t n_rows = (uint32_t)g.n_rows;
   const int bits = key_bits(g.n_rows);
-  const int passes = (int)cdiv(bits, kSortMaxBits), per = (int)cdiv(bits, passes), bins = 1 << per;
+  const int passes = (int)cdiv(bits, kSortMaxBits), per = std::max((int)cdiv(bits, passes), kSortMinBits), bins = 1 << per;
   const double row_bytes = (double)R * g.width * (g.dout_mode == ONETRANS_BF16 ? 2 : 4);
   ProfScope prof(PK_EMBEDDING_GRAD, (double)R * g.width,
                  row_bytes + (double)R * sizeof(Id) +
@@ -135,6 +139,7 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
     std::memset(&a, 0, sizeof(a));
     a.n_rows = n_rows;
     a.R = R;
+    a.tile = tile;
     a.tiles = tiles;
     a.bits = per;
     a.tot = hist + per_pass * passes;
@@ -143,23 +148,24 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
     a.scanned = tiles > kSortDirectTiles;
     launch_dependent(sort_hist_kernel<Id>, dim3(tiles), dim3(kSortThreads), 0, st, (const Id*)g.ids, a,
                      per_pass * (passes - 1));
-    const size_t smem = (size_t)kSortWarps * bins * 2 + (size_t)bins * 4;
-    if (!allow_smem(sort_pass_kernel<Id, true>, smem) || !allow_smem(sort_pass_kernel<Id, false>, smem))
-      return ONETRANS_ERR_CUDA;
-    for (int p = 0; p < passes; ++p) {
-      a.shift = p * per;
-      a.hist = hist + per_pass * p;
-      a.hist_next = p + 1 < passes ? a.hist + per_pass : nullptr;
-      if (a.scanned) launch_dependent(sort_scan_kernel, dim3((unsigned)cdiv(bins, 32)), dim3(1024), 0, st, a);
-      const uint32_t *ki = keys[at], *vi = vals[at];
-      if (p > 0) at ^= 1;
-      if (p == 0)
-        launch_dependent(sort_pass_kernel<Id, true>, dim3(tiles), dim3(kSortThreads), smem, st, (const Id*)g.ids,
-                         (const uint32_t*)nullptr, (const uint32_t*)nullptr, keys[at], vals[at], a, per, a.shift + per);
-      else
-        launch_dependent(sort_pass_kernel<Id, false>, dim3(tiles), dim3(kSortThreads), smem, st, (const Id*)nullptr, ki,
-                         vi, keys[at], vals[at], a, per, a.shift + per);
-    }
+    const size_t smem = (size_t)tile * 8 + (size_t)bins * 8 + (size_t)kSortWarps * bins * 2;
+    auto pass = [&](auto first, auto later) {
+      if (!allow_smem(first, smem) || !allow_smem(later, smem)) return ONETRANS_ERR_CUDA;
+      for (int p = 0; p < passes; ++p) {
+        a.shift = p * per;
+        a.hist = hist + per_pass * p;
+        a.hist_next = p + 1 < passes ? a.hist + per_pass : nullptr;
+        if (a.scanned) launch_dependent(sort_scan_kernel, dim3((unsigned)cdiv(bins, 32)), dim3(1024), 0, st, a);
+        const uint32_t *ki = keys[at], *vi = vals[at];
+        if (p > 0) at ^= 1;
+        launch_dependent(p == 0 ? first : later, dim3(tiles), dim3(kSortThreads), smem, st,
+                         p == 0 ? (const Id*)g.ids : nullptr, ki, vi, keys[at], vals[at], a, per, a.shift + per);
+      }
+      return ONETRANS_OK;
+    };
+    OT_TRY(items == 2   ? pass(sort_pass_kernel<Id, true, 2>, sort_pass_kernel<Id, false, 2>)
+           : items == 4 ? pass(sort_pass_kernel<Id, true, 4>, sort_pass_kernel<Id, false, 4>)
+                        : pass(sort_pass_kernel<Id, true, 8>, sort_pass_kernel<Id, false, 8>));
     if (!dense)
       launch_dependent(emb_heads_kernel, dim3(chunks), dim3(256), 0, st, (const uint32_t*)keys[at], R, n_rows, chunk,
                        heads);
