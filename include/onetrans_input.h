@@ -133,8 +133,9 @@ typedef struct {
  *   dweights [R, k] float32 or NULL (0 where a choice is none);
  *   grads: every weight gradient (zeros for a behaviour without events).
  * BF16 mode: float32 dtokens are rounded to bf16 as matrix operands; z and
- * the pre-activation gradient enter their products as two bf16 terms (16
- * bits of significand), so the weight gradients keep float32 quality.  R = 0
+ * the pre-activation gradient enter the weight gradients' products as two
+ * bf16 terms (16 bits of significand), so those keep float32 quality, and the
+ * event gradient's product as one.  R = 0
  * writes the zeros of grads.  The plan is checked as above. */
 ONETRANS_API onetrans_status onetrans_tokenize_routed_backward(
     const onetrans_model* m, const void* events, const float* weights, int64_t R, int32_t k, const void* plan,

@@ -9,8 +9,9 @@ of that element's sum (every operand replaced by its absolute value):
     slope by at most 2^-20 * (1 + |u|) in the accurate form.
   bf16 forward: z rounded to bf16 (2^-8 |z|), with a tanh good to 2^-10.9
     (2^-11.9 |u| of z), and the token rounded once (2^-8 of it).
-  bf16 backward: z and du as two bf16 terms (2^-16 of them).  float32 dtokens
-    are rounded to bf16 on entry: the reference takes the rounded values,
+  bf16 backward: z and du as two bf16 terms (2^-16 of them) for the weight
+    gradients, du as one (2^-8) for the event gradient.  float32 dtokens are
+    rounded to bf16 on entry: the reference takes the rounded values,
     except in dw's <dtoken, b2 + emb> (2^-8 of those terms)."""
 import numpy as np
 import pytest
@@ -116,7 +117,8 @@ def backward_ref(W, ev, types, wt, dy, dy_in, mode):
             edu = w.abs() * (edz * 1.2 + dz.abs() * eu * 1.3) + du.abs() * (split + 4 * u23)
             ez = eu * 1.3 + z.abs() * (split + 4 * u23)
             de.index_add_(0, r, du @ W1)
-            tde.index_add_(0, r, edu @ W1.abs() + (du.abs() @ W1.abs()) * (2 * d + 2) * u23)
+            one = 2.0 ** -8 * 1.01 if mode == "bf16" else 0.0
+            tde.index_add_(0, r, (edu + du.abs() * one) @ W1.abs() + (du.abs() @ W1.abs()) * (2 * d + 2) * u23)
             dw[r, j] = (dz * z).sum(1) + (dy_in[r].double() * s).sum(1)
             tdw[r, j] = ((edz * z.abs() + dz.abs() * ez).sum(1) + (dz * z).abs().sum(1) * (d + 8) * u23
                          + (dy_in[r].double().abs() * (s.abs() + 0.4)).sum(1) * (d + 8) * u23)

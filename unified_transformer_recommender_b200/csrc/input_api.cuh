@@ -389,6 +389,25 @@ static int weight_slices(long long tiles, int blocks, int waves) {
   return (int)std::max<long long>(1, std::min<long long>(tiles, cdiv(148 * waves, blocks)));
 }
 
+static onetrans_status wsum_launch(const PlanView& plan, const WeightPieces& w1, const WeightPieces& w2, int d, int e,
+                                   int T, const RoutedGrads& g, cudaStream_t st) {
+  const int v = d % 4 == 0 && e % 4 == 0 ? 4 : 1;
+  const dim3 grid((unsigned)std::min<long long>(cdiv(w1.stride + w2.stride, 256 * v), 1024), T);
+  if (v == 4) launch_dependent(routed_wsum_kernel<4>, grid, dim3(256), 0, st, plan, w1, w2, d, e, g);
+  else launch_dependent(routed_wsum_kernel<1>, grid, dim3(256), 0, st, plan, w1, w2, d, e, g);
+  return last_launch();
+}
+
+template <typename T, typename Td>
+static onetrans_status dweight_launch(const PlanView& plan, const RoutedMLP& mlp, int d, const void* dtokens,
+                                      const TokenRows& rows, const float* dot, int parts, float* dweights,
+                                      cudaStream_t st) {
+  const long long n = (long long)plan.R * plan.k;
+  launch_dependent(routed_dweight_kernel<T, Td>, dim3((unsigned)std::min<long long>(cdiv(n, 8), 148 * 8)), dim3(256), 0,
+                   st, plan, mlp, d, (const Td*)dtokens, rows, dot, parts, dweights);
+  return last_launch();
+}
+
 template <typename T, typename Td>
 static onetrans_status routed_backward_simt(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
                                             size_t ws_bytes, cudaStream_t st, size_t* need) {
@@ -396,10 +415,12 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   const long long cap = plan_buf(m, nullptr, R, k).cap, tiles = cap / 128;
   const int nb = (int)cdiv(d, 64), eb = (int)cdiv(e, 64);
   const int n2 = nb * nb, n1 = nb * eb;
-  WeightPieces w;
-  w.slices = weight_slices(tiles, n2 + n1, 4);
-  w.per = (int)cdiv(tiles, w.slices);
-  w.stride = (long long)d * d + (long long)d * e + 2 * d;
+  WeightPieces w1, w2;
+  w1.slices = weight_slices(tiles, n2 + n1, 4);
+  w1.per = (int)cdiv(tiles, w1.slices);
+  w2 = w1;
+  w1.stride = (long long)d * e + d;
+  w2.stride = (long long)d * d + d;
   Carve cv(ws, ws_bytes);
   RoutedArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -407,7 +428,8 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   a.buf0 = (float*)cv.take((size_t)cap * d * 4);
   a.buf1 = (float*)cv.take((size_t)cap * d * 4);
   a.dot = (float*)cv.take((size_t)cap * nb * 4);
-  w.part = (float*)cv.take((size_t)(w.slices + T_n) * w.stride * 4);
+  w1.part = (float*)cv.take((size_t)(w1.slices + T_n) * w1.stride * 4);
+  w2.part = (float*)cv.take((size_t)(w2.slices + T_n) * w2.stride * 4);
   if (need) {
     *need = cv.used;
     return ONETRANS_OK;
@@ -421,21 +443,16 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   const unsigned gy = (unsigned)(cap / 64);
   launch_dependent(routed_simt_kernel<T, Td, RS_HIDDEN_GRAD>, dim3(nb, gy), dim3(256), 0, st, a);
   launch_dependent(routed_simt_kernel<T, Td, RS_DU>, dim3(nb, gy), dim3(256), 0, st, a);
-  launch_dependent(routed_wgrad_simt_kernel<T, Td>, dim3(n2 + n1, w.slices), dim3(256), 0, st, a, w, n2);
-  launch_dependent(routed_wsum_kernel, dim3((unsigned)std::min<long long>(cdiv(w.stride, 256), 1024), T_n), dim3(256),
-                   0, st, a.plan, w, d, e, c->grads);
+  launch_dependent(routed_wgrad_simt_kernel<T, Td>, dim3(n2 + n1, w1.slices), dim3(256), 0, st, a, w1, w2, n2);
   OT_TRY(last_launch());
+  OT_TRY(wsum_launch(a.plan, w1, w2, d, e, T_n, c->grads, st));
   if (c->devents) {
     launch_dependent(routed_simt_kernel<T, Td, RS_DEVENT>, dim3(eb, gy), dim3(256), 0, st, a);
     OT_TRY(last_launch());
     OT_TRY(combine_launch<T>(a.plan, a.part, e, c->devents, TokenRows{0x7fffffff, 0}, st));
   }
-  if (c->dweights) {
-    launch_dependent(routed_dweight_kernel<T, Td>, dim3((unsigned)std::min<long long>(cdiv(R * k, 8), 148 * 8)),
-                     dim3(256), 0, st, a.plan, a.mlp, d, (const Td*)c->dtokens, c->rows, (const float*)a.dot, nb,
-                     c->dweights);
-    OT_TRY(last_launch());
-  }
+  if (c->dweights)
+    return dweight_launch<T, Td>(a.plan, a.mlp, d, c->dtokens, c->rows, a.dot, nb, c->dweights, st);
   return ONETRANS_OK;
 }
 
@@ -444,16 +461,21 @@ static onetrans_status routed_backward_tc(const onetrans_model* m, const RoutedC
   const int d = m->d, e = m->cfg.event_dim, T = m->cfg.n_behaviors;
   const long long cap = plan_buf(m, nullptr, R, k).cap, tiles = cap / 128;
   const WgCfg wc = wg_cfg(e, d);
-  WeightPieces w;
-  w.slices = (int)std::max<long long>(1, std::min<long long>(tiles, 148 / wc.roles));
-  w.per = (int)cdiv(tiles, w.slices);
-  w.stride = (long long)d * d + (long long)d * e + 2 * d;
+  WgArgs w;
+  std::memset(&w, 0, sizeof(w));
+  // both roles of every hidden chunk on the GPU's 148 SMs at once
+  w.p1.slices = (int)std::max<long long>(1, std::min<long long>(tiles, 74 / wc.chunks));
+  w.p1.per = (int)cdiv(tiles, w.p1.slices);
+  w.p2 = w.p1;
+  w.p1.stride = (long long)d * e + d;
+  w.p2.stride = (long long)d * d + d;
   Carve cv(ws, ws_bytes);
+  w.p1.part = (float*)cv.take((size_t)(w.p1.slices + T) * w.p1.stride * 4);
+  w.p2.part = (float*)cv.take((size_t)(w.p2.slices + T) * w.p2.stride * 4);
+  w.du = (__nv_bfloat16*)cv.take((size_t)cap * d * 2);
+  w.dot = (float*)cv.take((size_t)cap * wc.chunks * 4 * 4);
   float* part = k > 1 ? (float*)cv.take((size_t)R * k * e * 4) : nullptr;
-  w.part = (float*)cv.take((size_t)(w.slices + T) * w.stride * 4);
-  // float32 dtokens as bf16 rows
-  __nv_bfloat16* rounded =
-      !c || c->dtokens_mode == ONETRANS_FP32 ? (__nv_bfloat16*)cv.take((size_t)R * d * 2) : nullptr;
+  __nv_bfloat16* rounded = (__nv_bfloat16*)cv.take((size_t)R * d * 2);   // of float32 dtokens
   if (need) {
     *need = cv.used;
     return ONETRANS_OK;
@@ -469,35 +491,44 @@ static onetrans_status routed_backward_tc(const onetrans_model* m, const RoutedC
   a.events = (const __nv_bfloat16*)c->events; a.weights = c->weights;
   a.dtokens = (const __nv_bfloat16*)c->dtokens; a.rows = c->rows;
   a.devents = k == 1 ? (__nv_bfloat16*)c->devents : nullptr;
-  a.part = k > 1 && c->devents ? part : nullptr;
-  a.dweights = c->dweights;
+  a.part = k > 1 ? part : nullptr;
   ProfScope prof(PK_ROUTED_GRAD, 2.0 * R * k * (3.0 * e * d + 2.0 * d * d), (double)R * (2 * e + d) * m->es, st);
-  if (rounded) {
+  const bool f32 = c->dtokens_mode == ONETRANS_FP32;
+  if (f32) {
     launch_dependent(routed_round_rows_kernel, dim3((unsigned)std::min<long long>(cdiv(R * (d / 8), 256), 148 * 8)),
                      dim3(256), 0, st, (const float*)c->dtokens, c->rows, (int)R, d, rounded);
     OT_TRY(last_launch());
     a.dtokens = rounded;
     a.rows = TokenRows{0x7fffffff, 0};
   }
+  if (!c->devents) w.du = nullptr;
+  if (!c->dweights) w.dot = nullptr;
+  const dim3 grid(wc.chunks * (w.p1.slices + w.p2.slices));
   OT_TRY(by_chunks(d, [&](auto nc) {
     constexpr int NC = decltype(nc)::value;
-    if (!allow_smem(routed_wgrad_kernel<NC>, wc.smem)) return ONETRANS_ERR_CUDA;
-    launch_dependent(routed_wgrad_kernel<NC>, dim3(wc.roles * w.slices), dim3(kWgThreads), wc.smem, st, *maps, a, w);
-    return last_launch();
+    auto go = [&](auto kernel) {
+      if (!allow_smem(kernel, wc.smem)) return ONETRANS_ERR_CUDA;
+      launch_dependent(kernel, grid, dim3(kWgThreads), wc.smem, st, *maps, a, w);
+      return last_launch();
+    };
+    return w.dot ? go(routed_wgrad_kernel<NC, true>) : go(routed_wgrad_kernel<NC, false>);
   }));
-  launch_dependent(routed_wsum_kernel, dim3((unsigned)std::min<long long>(cdiv(w.stride, 256), 1024), T), dim3(256), 0,
-                   st, a.plan, w, d, e, c->grads);
-  OT_TRY(last_launch());
-  if (!c->devents && !c->dweights) return ONETRANS_OK;
-  const int smem = dev_cfg(e, d).smem;
-  OT_TRY(by_chunks(d, [&](auto nc) {
-    constexpr int NC = decltype(nc)::value;
-    if (!allow_smem(routed_devents_kernel<NC>, smem)) return ONETRANS_ERR_CUDA;
-    launch_dependent(routed_devents_kernel<NC>, dim3((unsigned)std::min<long long>(tiles, device_sm_count())),
-                     dim3(kTokThreads), smem, st, *maps, a);
-    return last_launch();
-  }));
-  return a.part ? combine_launch<__nv_bfloat16>(a.plan, part, e, c->devents, TokenRows{0x7fffffff, 0}, st) : ONETRANS_OK;
+  OT_TRY(wsum_launch(a.plan, w.p1, w.p2, d, e, T, c->grads, st));
+  if (c->devents) {
+    const int smem = dev_cfg(e, d).smem;
+    OT_TRY(by_chunks(d, [&](auto nc) {
+      constexpr int NC = decltype(nc)::value;
+      if (!allow_smem(routed_devents_kernel<NC>, smem)) return ONETRANS_ERR_CUDA;
+      launch_dependent(routed_devents_kernel<NC>, dim3((unsigned)std::min<long long>(tiles, device_sm_count())),
+                       dim3(kDevThreads), smem, st, *maps, a, (const __nv_bfloat16*)w.du);
+      return last_launch();
+    }));
+    if (part) OT_TRY(combine_launch<__nv_bfloat16>(a.plan, part, e, c->devents, TokenRows{0x7fffffff, 0}, st));
+  }
+  if (!c->dweights) return ONETRANS_OK;
+  return f32 ? dweight_launch<__nv_bfloat16, float>(a.plan, a.mlp, d, c->dtokens, c->rows, w.dot, wc.chunks * 4, c->dweights, st)
+             : dweight_launch<__nv_bfloat16, __nv_bfloat16>(a.plan, a.mlp, d, c->dtokens, c->rows, w.dot, wc.chunks * 4,
+                                                            c->dweights, st);
 }
 
 static onetrans_status tokenize_routed_any(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(256) routed_dweight_kernel(PlanView plan, Rout
 struct WeightPieces {
   int per, slices;
   float* part;           // [slices + T - 1][stride]
-  long long stride;      // floats of one piece: dW2 [d][d], dW1 [d][e], db1 [d], db2 [d]
+  long long stride;      // floats of one piece: a weight gradient, then its bias's
 };
 __device__ inline float* piece_at(const WeightPieces& w, int s, int t) { return w.part + (long long)(s + t) * w.stride; }
 
@@ -399,7 +399,8 @@ __device__ inline float* piece_at(const WeightPieces& w, int s, int t) { return 
 // one slice, behaviour after behaviour.  The CTAs of the first column block
 // also add up db2 (dW2) or db1 (dW1) of their 64 rows.
 template <typename T, typename Td>
-__global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, WeightPieces w, int n2) {
+__global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, WeightPieces w1, WeightPieces w2,
+                                                                int n2) {
   __shared__ __align__(16) float As[16][68], Bs[16][68];
   grid_dep_wait();
   grid_dep_launch();
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, We
   const int k = a.plan.k;
   const int lr = threadIdx.x >> 4, lc = (threadIdx.x & 15) * 4;   // slot, 4 columns
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const WeightPieces& w = second ? w2 : w1;
   const int tile0 = blockIdx.y * w.per, tile1 = min(tile0 + w.per, plan_first(a.plan, a.plan.T) / 128);
   for (int t = 0; t < a.plan.T; ++t) {
     const int first = plan_first(a.plan, t);
@@ -453,8 +455,7 @@ __global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, We
       if (c0 == 0 && threadIdx.x < 64)
         for (int kk = 0; kk < 16; ++kk) colsum = fmaf(As[kk][threadIdx.x], Bs[kk][64], colsum);
     }
-    float* p = piece_at(w, blockIdx.y, t);
-    float* mat = second ? p : p + (long long)a.d * a.d;
+    float* mat = piece_at(w, blockIdx.y, t);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -462,10 +463,7 @@ __global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, We
         const int m = m0 + ty * 4 + i, c = c0 + tx * 4 + j;
         if (m < a.d && c < cols) mat[(long long)m * cols + c] = acc[i][j];
       }
-    if (c0 == 0 && threadIdx.x < 64 && m0 + threadIdx.x < a.d) {
-      float* bias = p + (long long)a.d * (a.d + a.e) + (second ? a.d : 0);
-      bias[m0 + threadIdx.x] = colsum;
-    }
+    if (c0 == 0 && threadIdx.x < 64 && m0 + threadIdx.x < a.d) mat[(long long)a.d * cols + m0 + threadIdx.x] = colsum;
   }
 }
 
@@ -475,26 +473,57 @@ struct RoutedGrads {
 };
 
 // Each behaviour's pieces added in slice order (zeros where it has none);
-// blockIdx.y = behaviour, four neighbouring values per thread where the piece
-// allows it.
-__global__ void __launch_bounds__(256) routed_wsum_kernel(PlanView plan, WeightPieces w, int d, int e, RoutedGrads g) {
+// blockIdx.y = behaviour, V neighbouring values a thread, eight pieces in
+// flight.  p1: dW1 and db1, p2: dW2 and db2.
+template <int V>
+__global__ void __launch_bounds__(256) routed_wsum_kernel(PlanView plan, WeightPieces p1, WeightPieces p2, int d, int e,
+                                                          RoutedGrads g) {
   grid_dep_wait();
   grid_dep_launch();
   if (!plan_ok(plan)) return;
   const int t = blockIdx.y;
   const int tile0 = plan_first(plan, t) / 128, tile1 = plan_first(plan, t + 1) / 128;
-  const int s0 = tile0 / w.per, s1 = tile1 > tile0 ? (tile1 - 1) / w.per + 1 : s0;
-  const long long n2 = (long long)d * d, n1 = (long long)d * e;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < w.stride; i += (long long)gridDim.x * 256) {
-    float s = 0.f;
-#pragma unroll 8
-    for (int q = s0; q < s1; ++q) s += piece_at(w, q, t)[i];
-    if (i < n2) g.W2[t][i] = s;
-    else if (i < n2 + n1) g.W1[t][i - n2] = s;
-    else if (i < n2 + n1 + d) g.b1[t][i - n2 - n1] = s;
-    else {
-      g.b2[t][i - n2 - n1 - d] = s;
-      g.emb[(long long)t * d + (i - n2 - n1 - d)] = s;
+  const long long n1 = (long long)d * e, n2 = (long long)d * d;
+  for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * V; i < p1.stride + p2.stride;
+       i += (long long)gridDim.x * 256 * V) {
+    const bool one = i < p1.stride;
+    const WeightPieces& w = one ? p1 : p2;
+    const long long j = one ? i : i - p1.stride;
+    const int s0 = tile0 / w.per, s1 = tile1 > tile0 ? (tile1 - 1) / w.per + 1 : s0;
+    float s[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) s[k] = 0.f;
+    for (int q0 = s0; q0 < s1; q0 += 8) {
+      float v[8][V];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float* p = piece_at(w, q0 + q, t) + j;
+        if (q0 + q >= s1) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[q][k] = 0.f;
+        } else if constexpr (V == 4) {
+          const float4 x = *(const float4*)p;
+          v[q][0] = x.x; v[q][1] = x.y; v[q][2] = x.z; v[q][3] = x.w;
+        } else {
+          v[q][0] = *p;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int k = 0; k < V; ++k) s[k] += v[q][k];
+    }
+    auto put = [&](float* o) {
+      if constexpr (V == 4) *(float4*)o = make_float4(s[0], s[1], s[2], s[3]);
+      else *o = s[0];
+    };
+    if (one) {
+      put(j < n1 ? g.W1[t] + j : g.b1[t] + (j - n1));
+    } else if (j < n2) {
+      put(g.W2[t] + j);
+    } else {
+      put(g.b2[t] + (j - n2));
+      put(g.emb + (long long)t * d + (j - n2));
     }
   }
 }

@@ -21,9 +21,8 @@ struct RoutedTcArgs {
   __nv_bfloat16* tokens;         // k = 1
   // gradient
   const __nv_bfloat16* dtokens;
-  __nv_bfloat16* devents;        // k = 1, or null
-  float* dweights;               // [R*k] or null
-  float* part;                   // k > 1: [R*k][d] of the tokens, [R*k][e] of the event gradient (or null)
+  __nv_bfloat16* devents;        // k = 1
+  float* part;                   // k > 1: [R*k][d] of the tokens, [R*k][e] of the event gradient
 };
 
 constexpr int kSmemMax = 232448;
@@ -163,18 +162,21 @@ __device__ inline void load_biases(float* to, const RoutedMLP& mlp, int t, int d
 // One CTA per SM walks 128-slot tiles.  Per 64 hidden units: U = E W1c^T
 // (tcgen05, M = 128, N = 64), bias and GELU by eight warps, z packed to bf16
 // over U's own TMEM columns, D += z W2c^T with z read from TMEM (N = d).  The
-// hidden row therefore never leaves the SM.  Two U buffers let the next
-// chunk's first product run during this one's GELU; the weights stream
-// through a ring (the tiles of one behaviour read the same 2 d (e + d) bytes,
-// which stay in L2).  The gathered event rows come through cp.async into the
+// hidden row therefore never leaves the SM.  A chunk's weights and its U
+// columns form one slot of a ring: both are free when its second product is
+// done, so the chain product - GELU - product of up to four chunks overlaps
+// (one chunk's chain takes about 2000 cycles, its products 800).  The weights
+// stream through that ring from L2 (the tiles of one behaviour read the same
+// 2 d (e + d) bytes).  The gathered event rows come through cp.async into the
 // swizzled operand layout; four warps of their own take D out, weighted, as
 // 128-byte pieces of the destination rows, while the next tile's first
 // hidden units are computed.
-// Warps 0-7 GELU, 8-11 output, 12-15 gather, 16 weights, 17 products.
-constexpr int kTokThreads = 576, kTokGelu = 8, kTokOut = 4;
+// Warps 0-7 GELU, 8-11 output, 12-15 gather, 16 weights, 17 first products,
+// 18 second products (one issuing warp would be the bottleneck).
+constexpr int kTokThreads = 608, kTokGelu = 8, kTokOut = 4;
 
 struct TokCfg {
-  int ebuf, stages;               // event tiles and weight stages in flight
+  int ebuf, slots;                // event tiles in flight, ring slots
   int e_bytes, w1_bytes, stage_bytes, smem;
 };
 __host__ __device__ inline TokCfg tok_cfg(int e, int d) {
@@ -187,9 +189,11 @@ __host__ __device__ inline TokCfg tok_cfg(int e, int d) {
   const int fixed = kTokOut * 32 * 144 + 4 * d * 4 + 128 * 4 + 512;
   const int room = kSmemMax - fixed;
   c.ebuf = eb == 1 ? 2 : 1;
-  c.stages = (room - c.ebuf * c.e_bytes) / c.stage_bytes;
-  if (c.stages > 4) c.stages = 4;
-  c.smem = fixed + c.ebuf * c.e_bytes + c.stages * c.stage_bytes;
+  c.slots = (room - c.ebuf * c.e_bytes) / c.stage_bytes;
+  const int cols = (512 - d) / 64;                // U buffers beside D in TMEM
+  if (c.slots > cols) c.slots = cols;
+  if (c.slots > 4) c.slots = 4;
+  c.smem = fixed + c.ebuf * c.e_bytes + c.slots * c.stage_bytes;
   return c;
 }
 
@@ -201,23 +205,22 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   const TokCfg cfg = tok_cfg(a.e, d);
   uint8_t* sE = smem;
   uint8_t* sW = sE + cfg.ebuf * cfg.e_bytes;
-  uint8_t* sOut = sW + cfg.stages * cfg.stage_bytes;
+  uint8_t* sOut = sW + cfg.slots * cfg.stage_bytes;
   float* sBias = (float*)(sOut + kTokOut * 32 * 144);       // [2][2 d]
   int* sRow = (int*)(sBias + 4 * d);                        // [128]
   uint64_t* bars = (uint64_t*)(sRow + 128);
   uint64_t* e_full = bars;          // [2]
   uint64_t* e_empty = bars + 2;     // [2]
-  uint64_t* w_full = bars + 4;      // [4]
-  uint64_t* w_empty = bars + 8;     // [4]
-  uint64_t* u_full = bars + 12;     // [2]
-  uint64_t* z_ready = bars + 14;    // [2]
-  uint64_t* dn_done = bars + 16;    // [2]
-  uint64_t* b_free = bars + 18;     // [2]: a tile's biases have been used
-  uint64_t* d_full = bars + 20;
-  uint64_t* d_empty = bars + 21;
-  uint64_t* b_full = bars + 22;     // [2]
-  uint32_t* tmem_slot = (uint32_t*)(bars + 24);
-  PlanSpans* spans = (PlanSpans*)(bars + 26);
+  uint64_t* w_full = bars + 4;      // [4] a slot's weights
+  uint64_t* u_full = bars + 8;      // [4]
+  uint64_t* z_ready = bars + 12;    // [4]
+  uint64_t* slot_free = bars + 16;  // [4]
+  uint64_t* b_full = bars + 20;     // [2] a tile's biases
+  uint64_t* b_free = bars + 22;     // [2]
+  uint64_t* d_full = bars + 24;
+  uint64_t* d_empty = bars + 25;
+  uint32_t* tmem_slot = (uint32_t*)(bars + 26);
+  PlanSpans* spans = (PlanSpans*)(bars + 28);
 
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) flag_error(kErrSmemAlign);
@@ -228,15 +231,14 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&e_full[i], 4);
       mbar_init(&e_empty[i], 1);
-      mbar_init(&u_full[i], 1);
-      mbar_init(&z_ready[i], kTokGelu);
-      mbar_init(&dn_done[i], 1);
       mbar_init(&b_full[i], 4);
       mbar_init(&b_free[i], kTokGelu + kTokOut);
     }
-    for (int i = 0; i < cfg.stages; ++i) {
+    for (int i = 0; i < cfg.slots; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 1);
+      mbar_init(&u_full[i], 1);
+      mbar_init(&z_ready[i], kTokGelu);
+      mbar_init(&slot_free[i], 1);
     }
     mbar_init(d_full, 1);
     mbar_init(d_empty, kTokOut);
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tD = tmem, tU = tmem + 384;   // U buffers at 384 and 448
+  const uint32_t tD = tmem, tU = tmem + d;   // U of slot s at tU + 64 s
   grid_dep_wait();
   grid_dep_launch();
   const bool fine = load_spans(a.plan, spans);
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       for (int tile = blockIdx.x; tile < n_tiles && ok; tile += step) {
         const int t = span_type(spans, T, tile * 128);
         for (int c = 0; c < NC; ++c) {
-          ok = !wrapped || mbar_wait(&w_empty[w.s], w.ph ^ 1);
+          ok = !wrapped || mbar_wait(&slot_free[w.s], w.ph ^ 1);
           if (!ok) break;
           uint8_t* w1 = sW + w.s * cfg.stage_bytes;
           mbar_expect_tx(&w_full[w.s], cfg.stage_bytes);
@@ -272,69 +274,61 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
           for (int b = 0; b < NC; ++b)
             tma_load_3d_hint(&maps.w2[t], &w_full[w.s], w1 + cfg.w1_bytes + b * 8192, c * 64, b * 64, 0, keep);
-          w.next(cfg.stages);
+          w.next(cfg.slots);
           wrapped = wrapped || w.s == 0;
         }
       }
     }
   } else if (warp == 17) {
-    // ------------------------------------------------------------- products
-    {
-      const uint64_t dE = sdesc_k128(smem_u32(sE)), dW = sdesc_k128(smem_u32(sW));
-      constexpr uint32_t id_u = idesc_bf16(128, 64);
-      constexpr int n0 = d > 256 ? 256 : d, n1 = d - n0;
-      constexpr uint32_t id_0 = idesc_bf16(128, n0), id_1 = idesc_bf16(128, n1 ? n1 : 16);
-      const int ksteps = a.e / 16;
-      const int mine = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - (int)blockIdx.x) / step + 1 : 0;
-      const int total = mine * NC;
-      bool ok = true;
-      RingPos wu, wd, eu;           // weight stage of the next up / down product, event tile of the next up
-      int gu = 0, cu = 0, cd = 0, tiles_done = 0;
-      auto up = [&]() {
-        ok = ok && mbar_wait(&w_full[wu.s], wu.ph);
-        if (cu == 0) ok = ok && mbar_wait(&e_full[eu.s], eu.ph);
-        if (gu >= 2) ok = ok && mbar_wait(&dn_done[gu & 1], ((gu >> 1) & 1) ^ 1);   // z of two chunks before consumed
-        if (!ok) return;
+    // ------------------------------------------------------- first products
+    const uint64_t dE = sdesc_k128(smem_u32(sE)), dW = sdesc_k128(smem_u32(sW));
+    constexpr uint32_t id_u = idesc_bf16(128, 64);
+    const int ksteps = a.e / 16;
+    bool ok = true;
+    RingPos r, er;
+    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += step) {
+      for (int c = 0; c < NC; ++c) {
+        ok = mbar_wait(&w_full[r.s], r.ph);      // refilled, so the slot's U is free too
+        if (c == 0) ok = ok && mbar_wait(&e_full[er.s], er.ph);
+        if (!ok) break;
         tc_fence_after();
-        const uint64_t de = desc_add(dE, eu.s * cfg.e_bytes), dw = desc_add(dW, wu.s * cfg.stage_bytes);
-        const uint32_t to = tU + (gu & 1) * 64;
+        const uint64_t de = desc_add(dE, er.s * cfg.e_bytes), dw = desc_add(dW, r.s * cfg.stage_bytes);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < ksteps)
-            mma_ss(to, desc_add(de, (k >> 2) * 16384 + (k & 3) * 32), desc_add(dw, (k >> 2) * 8192 + (k & 3) * 32), id_u,
-                      k ? 1u : 0u);
-        mma_commit(&u_full[gu & 1]);
-        if (++cu == NC) {
-          cu = 0;
-          mma_commit(&e_empty[eu.s]);
-          eu.next(cfg.ebuf);
-        }
-        wu.next(cfg.stages);
-        ++gu;
-      };
-      if (total > 0) up();
-      for (int g = 0; g < total && ok; ++g) {
-        if (g + 1 < total) up();
-        ok = ok && mbar_wait(&z_ready[g & 1], (g >> 1) & 1);
-        if (cd == 0 && tiles_done > 0) ok = ok && mbar_wait(d_empty, (tiles_done - 1) & 1);
+            mma_ss(tU + r.s * 64, desc_add(de, (k >> 2) * 16384 + (k & 3) * 32),
+                   desc_add(dw, (k >> 2) * 8192 + (k & 3) * 32), id_u, k ? 1u : 0u);
+        mma_commit(&u_full[r.s]);
+        r.next(cfg.slots);
+      }
+      mma_commit(&e_empty[er.s]);
+      er.next(cfg.ebuf);
+    }
+  } else if (warp == 18) {
+    // ------------------------------------------------------ second products
+    const uint64_t dW = sdesc_k128(smem_u32(sW) + cfg.w1_bytes);
+    constexpr int n0 = d > 256 ? 256 : d, n1 = d - n0;
+    constexpr uint32_t id_0 = idesc_bf16(128, n0), id_1 = idesc_bf16(128, n1 ? n1 : 16);
+    bool ok = true;
+    RingPos r;
+    int i = 0;
+    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += step, ++i) {
+      for (int c = 0; c < NC; ++c) {
+        ok = mbar_wait(&z_ready[r.s], r.ph);
+        if (c == 0 && i > 0) ok = ok && mbar_wait(d_empty, (i - 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t w2 = desc_add(dW, wd.s * cfg.stage_bytes + cfg.w1_bytes);
+        const uint64_t w2 = desc_add(dW, r.s * cfg.stage_bytes);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {   // units 16k .. 16k+15 packed over U columns 16k .. 16k+7
-          const uint32_t z = tU + (g & 1) * 64 + k * 16;
-          mma_ts(tD, z, desc_add(w2, k * 32), id_0, (cd | k) ? 1u : 0u);
-          if (n1) mma_ts(tD + n0, z, desc_add(w2, n0 * 128 + k * 32), id_1, (cd | k) ? 1u : 0u);
+          const uint32_t z = tU + r.s * 64 + k * 16;
+          mma_ts(tD, z, desc_add(w2, k * 32), id_0, (c | k) ? 1u : 0u);
+          if (n1) mma_ts(tD + n0, z, desc_add(w2, n0 * 128 + k * 32), id_1, (c | k) ? 1u : 0u);
         }
-        mma_commit(&w_empty[wd.s]);
-        mma_commit(&dn_done[g & 1]);
-        if (++cd == NC) {
-          cd = 0;
-          ++tiles_done;
-          mma_commit(d_full);
-        }
-        wd.next(cfg.stages);
+        mma_commit(&slot_free[r.s]);
+        r.next(cfg.slots);
       }
+      mma_commit(d_full);
     }
   } else if (warp >= 12) {
     // --------------------------------------------------------------- gather
@@ -418,18 +412,20 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   } else {
     // ----------------------------------------------------------------- GELU
     const int q4 = warp & 3, wq = warp >> 2;    // row quarter, half of the chunk's columns
-    const uint32_t col = tU + ((uint32_t)(q4 * 32) << 16) + wq * 32;
+    const uint32_t mine = tU + ((uint32_t)(q4 * 32) << 16) + wq * 32;
     bool ok = true;
-    int i = 0, g = 0;
+    RingPos r;
+    int i = 0;
     for (int tile = blockIdx.x; tile < n_tiles; tile += step, ++i) {
       const float* b1 = sBias + (i & 1) * 2 * d + wq * 32;
       ok = ok && mbar_wait(&b_full[i & 1], (i >> 1) & 1);
 #pragma unroll 1
-      for (int c = 0; c < NC; ++c, ++g) {
-        ok = ok && mbar_wait(&u_full[g & 1], (g >> 1) & 1);
+      for (int c = 0; c < NC; ++c) {
+        ok = ok && mbar_wait(&u_full[r.s], r.ph);
         tc_fence_after();
+        const uint32_t col = mine + r.s * 64;
         float v[32];
-        tmem_ld32(col + (g & 1) * 64, v);
+        tmem_ld32(col, v);
         uint32_t pk[16];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -437,11 +433,12 @@ __global__ void __launch_bounds__(kTokThreads, 1)
           pk[2 * j] = gelu_bias_bf16x2(v[4 * j], v[4 * j + 1], b.x, b.y);
           pk[2 * j + 1] = gelu_bias_bf16x2(v[4 * j + 2], v[4 * j + 3], b.z, b.w);
         }
-        tmem_st8(col + (g & 1) * 64, pk);
-        tmem_st8(col + (g & 1) * 64 + 16, pk + 8);
+        tmem_st8(col, pk);
+        tmem_st8(col + 16, pk + 8);
         tmem_st_wait();
         tc_fence_before();
-        warp_arrive(&z_ready[g & 1]);
+        warp_arrive(&z_ready[r.s]);
+        r.next(cfg.slots);
       }
       warp_arrive(&b_free[i & 1]);
     }
@@ -452,22 +449,49 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 }
 
 // ------------------------------------------------------- shared, backward --
-// GELU-tanh and its slope to float32 accuracy: with s = 1 / (1 + exp(-2v)),
-// v = c (u + a u^3), GELU(u) = u s and d/du = s + 2 u s (1 - s) c (1 + 3 a u^2)
-// (0.5 (1 + tanh v) = s).  Two special-function results per value (exp, the
-// reciprocal); |v| large gives s = 0 or 1 exactly.
-__device__ inline void gelu_and_slope_fast(float u, float& z, float& g) {
-  const float c = 0.7978845608028654f, a = 0.044715f;
-  const float u2 = u * u;
-  const float v = u * fmaf(c * a, u2, c);
-  const float s = __fdividef(1.f, 1.f + __expf(-2.f * v));
-  z = u * s;
-  // at |u| past 10 the second term is zero, but u2 * (1 - s) could be inf * 0
-  const float q = fmaf(6.f * c * a, u2, 2.f * c);
-  g = fabsf(u) < 16.f ? fmaf(z * (1.f - s), q, s) : s;
+__device__ inline float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-// x0, x1 as bf16 pairs hi + lo: 16 bits of significand in two operands.
-__device__ inline void split_bf16x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+__device__ inline float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// GELU-tanh and its slope of a pair, to float32 accuracy: with
+// s = 1 / (1 + exp(-2v)), v = c (u + a u^3), GELU(u) = u s and
+// d/du = s + u s (1 - s) (2c + 6 c a u^2)  (0.5 (1 + tanh v) = s).  Two
+// special-function results a value (16 a clock an SM, the bound of these
+// loops), the rest on packed float32 pairs.  |u| large gives s = 0 or 1
+// exactly; u^2 is bounded in the slope, where inf * 0 would follow.
+struct GeluPair {
+  uint64_t u2, s, z;
+};
+__device__ __forceinline__ GeluPair gelu_pair(uint64_t u) {
+  const float c = 0.7978845608028654f, a = 0.044715f, m2l = -2.8853900817779268f;   // -2 log2(e)
+  GeluPair r;
+  r.u2 = f2_mul(u, u);
+  const uint64_t v = f2_mul(u, f2_fma(r.u2, f2_pack(m2l * c * a, m2l * c * a), f2_pack(m2l * c, m2l * c)));
+  float x, y;
+  f2_unpack(v, x, y);
+  const uint64_t d = f2_add(f2_pack(ex2_ftz(x), ex2_ftz(y)), f2_pack(1.f, 1.f));
+  f2_unpack(d, x, y);
+  r.s = f2_pack(rcp_ftz(x), rcp_ftz(y));
+  r.z = f2_mul(u, r.s);
+  return r;
+}
+__device__ __forceinline__ uint64_t gelu_slope(const GeluPair& r) {
+  const float c = 0.7978845608028654f, a = 0.044715f;
+  float x, y;
+  f2_unpack(r.u2, x, y);
+  const uint64_t q = f2_fma(f2_pack(fminf(x, 256.f), fminf(y, 256.f)), f2_pack(6.f * c * a, 6.f * c * a), f2_pack(2.f * c, 2.f * c));
+  return f2_fma(f2_mul(r.z, f2_fma(r.s, f2_pack(-1.f, -1.f), f2_pack(1.f, 1.f))), q, r.s);
+}
+// A pair as bf16 hi + lo: 16 bits of significand in two operands.
+__device__ __forceinline__ void split_pair(uint64_t x, uint32_t& hi, uint32_t& lo) {
+  float x0, x1;
+  f2_unpack(x, x0, x1);
   hi = pack_bf16x2(x0, x1);
   lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
 }
@@ -490,252 +514,764 @@ __global__ void __launch_bounds__(256) routed_round_rows_kernel(const float* __r
   }
 }
 
-// ------------------------------------------------------------ event gradient --
-// de = W1^T du and dw, tile by tile like the forward: per 64 hidden units
-// U = E W1c^T (K = e) and DZ = DY W2c (K = d) into TMEM, du = w dz GELU'(u) by
-// eight warps, split into two bf16 terms over U's columns, DE += du W1c.
-// W1's chunk serves both of its products from one shared-memory tile (K-major
-// for U, MN-major for DE), as W2's does in the forward.  dw's row sums stay
-// with the threads that own the row.
-// Warps 0-7 GELU, 8-11 output, 12-15 gather, 16 weights, 17 products.
-struct DevCfg {
-  int abuf, units;                // row tiles in flight, W2 units of 64 rows
-  int a_bytes, w1_bytes, smem;
+// ----------------------------------------------------------- weight gradients --
+// A CTA holds 128 hidden units of one behaviour at a time and walks its slice
+// of the slots, 128 (one tile) a step, transposed so that hidden units are
+// TMEM lanes:
+//   U^T = W1c E^T (M = 128 units, N = 128 slots, K = e),
+//   DZ^T = W2c^T DY^T (K = d); then, from z and du in TMEM as A operands,
+//   dW2c^T [128][d] += z DY and dW1c [128][e] += du E (K = 128 slots).
+// z = w GELU(u) and du = w dz GELU'(u) overwrite the columns they come from
+// as two bf16 terms each, so the hidden rows are recomputed but never stored,
+// db1 is a sum inside a thread, and the gathered rows serve as both K-major
+// and MN-major operands.  Both gradients need U but nothing else of one
+// another, and together more TMEM than there is; so half of the CTAs (role 1)
+// compute U, DZ, du, dW1 and db1, the other half (role 2) U, z, dW2 and db2,
+// about 2400 tensor-core cycles a step (d = 256, e = 64) each.
+// Role 1 also writes du, rounded once to bf16, as rows for the event gradient
+// and, where asked, each slot's <dz, z> over its units.
+// Warps 0-15 compute, 16-19 gather, 20 loads weights, 21 first products, 22
+// second products.
+constexpr int kWgThreads = 736, kWgCompute = 16;
+
+struct WgCfg {
+  int eb, chunks;                  // event boxes, hidden chunks of 128
+  int w1_bytes, e_bytes;
+  int units1, units2;              // DY ring: role 1 [128 slots x 64], role 2 [64 slots x d]
+  int ring;                        // bytes behind the event tiles
+  int smem;
 };
-constexpr int kDevW1 = 2;         // W1 stages
+__host__ __device__ inline WgCfg wg_cfg(int e, int d) {
+  WgCfg c;
+  c.eb = (e + 63) / 64;
+  c.chunks = (d + 127) / 128;
+  c.w1_bytes = c.eb * 16384;
+  c.e_bytes = c.eb * 16384;
+  const int fixed = 512 + 2 * 128 * 16;   // barriers and spans; row offsets, indices and weights of two steps
+  const int room = kSmemMax - fixed - c.w1_bytes - 2 * c.e_bytes;
+  c.units1 = (room - d * 256) / 16384;
+  if (c.units1 > 8) c.units1 = 8;
+  c.units2 = room / (d * 128);
+  if (c.units2 > 8) c.units2 = 8;
+  const int s1 = d * 256 + c.units1 * 16384, s2 = c.units2 * d * 128;
+  c.ring = s1 > s2 ? s1 : s2;
+  c.smem = fixed + c.w1_bytes + 2 * c.e_bytes + c.ring;
+  return c;
+}
+
+struct WgArgs {
+  WeightPieces p1, p2;           // dW1 [d][e] and db1 [d]; dW2 [d][d] and db2 [d]
+  __nv_bfloat16* du;             // [slots][d], or null
+  float* dot;                    // [slots][4 chunks], or null
+};
+
+struct WgShared {                // one CTA's shared memory
+  uint8_t *w1, *e, *w2, *y;      // w2: role 1; y: the DY ring
+  long long* off;                // [2][128] dtoken rows
+  int* row;                      // [2][128] event rows
+  float* wt;                     // [2][128] choice weights
+  uint64_t* bars;
+  PlanSpans* spans;
+};
+enum : int {   // barriers; pairs and rings by index
+  WB_EFULL = 0, WB_EEMPTY = 2, WB_YFULL = 4, WB_YEMPTY = 12, WB_UFULL = 20, WB_UFREE = 22, WB_ZFULL = 24, WB_READY = 26,
+  WB_USED = 28, WB_W = 30, WB_ACCFULL = 31, WB_ACCFREE = 32, WB_TMEM = 33, WB_SPANS = 34
+};
+
+// The slots of behaviour t in tiles [tile0, tile1): [lo, hi), hi before the padding.
+__device__ inline bool wg_piece(const PlanSpans* s, int tile0, int tile1, int t, int& lo, int& hi) {
+  lo = max(tile0 * 128, s->first[t]);
+  hi = min(tile1 * 128, s->first[t] + s->cnt[t]);
+  return lo < hi;
+}
+
+// Gathers the steps' event tiles and DY units.  A load's copies stay in flight
+// while up to depth - 1 newer loads are issued; its arrival follows then.
+// depth is below the ring's size and a step's loads, so that no load waits for
+// a slot that only an arrival still held back could free.
+template <int NC, bool ROLE1>
+__device__ inline void wg_gather(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, int tile0, int tile1) {
+  constexpr int d = NC * 64;
+  const int tid = threadIdx.x - kWgCompute * 32, units = ROLE1 ? cfg.units1 : cfg.units2;
+  const int depth = min(min(3, units - 1), ROLE1 ? NC + 1 : 3);
+  bool ok = true, wrapped = false;
+  int i = 0, pending = 0, pend0 = 0, pend1 = 0, pend2 = 0;   // barriers of the loads in flight, oldest first
+  RingPos y;
+  auto arrive = [&]() {          // the oldest load's copies are done
+    fence_async_smem();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    warp_arrive(&m.bars[pend0]);
+    pend0 = pend1;
+    pend1 = pend2;
+    --pending;
+  };
+  auto issued = [&](int bar) {
+    cp_async_commit();
+    if (pending == 0) pend0 = bar;
+    else if (pending == 1) pend1 = bar;
+    else pend2 = bar;
+    if (++pending < depth) return;
+    if (depth == 3) cp_async_wait<2>();
+    else if (depth == 2) cp_async_wait<1>();
+    else cp_async_wait<0>();
+    arrive();
+  };
+  for (int t = 0; t < a.plan.T; ++t) {
+    int lo, hi;
+    if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+    int flat = lo + tid < hi ? a.plan.order[lo + tid] : -1;
+    for (int at = lo; at < hi; at += 128, ++i) {
+      const int b = i & 1;
+      const int row = flat < 0 ? -1 : flat / a.plan.k;
+      const float wt = flat < 0 ? 0.f : a.weights ? a.weights[flat] : 1.f;
+      flat = at + 128 + tid < hi ? a.plan.order[at + 128 + tid] : -1;   // of the next step
+      if (i >= 2) ok = ok && mbar_wait(&m.bars[WB_EEMPTY + b], ((i >> 1) & 1) ^ 1);
+      m.off[b * 128 + tid] = row < 0 ? -1LL : token_off(a.rows, row, d);
+      m.row[b * 128 + tid] = row;
+      m.wt[b * 128 + tid] = wt;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (ok) gather_events<128>(m.e + b * cfg.e_bytes, m.row + b * 128, 128, a.e, a.events, tid);
+      issued(WB_EFULL + b);
+      const long long* off = m.off + b * 128;
+#pragma unroll 1
+      for (int u = 0; u < (ROLE1 ? NC : 2); ++u) {
+        if (wrapped) ok = ok && mbar_wait(&m.bars[WB_YEMPTY + y.s], y.ph ^ 1);
+        if (ok && ROLE1)
+          gather_boxes<128, 1>(m.y + y.s * 16384, [&](int r) { return off[r] < 0 ? -1LL : off[r] + u * 64; }, 128, 64,
+                               a.dtokens, tid);
+        if (ok && !ROLE1)
+          gather_boxes<128, NC>(m.y + y.s * (d * 128), [&](int r) { return off[u * 64 + r]; }, 64, d, a.dtokens, tid);
+        issued(WB_YFULL + y.s);
+        y.next(units);
+        wrapped = wrapped || y.s == 0;
+      }
+    }
+  }
+  cp_async_wait<0>();
+  while (pending > 0) arrive();
+}
+
+// Role 1's products.
+template <int NC>
+__device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, uint32_t tmem, int tile0,
+                                    int tile1, bool first) {
+  constexpr int d = NC * 64;
+  const uint32_t tU = tmem, tZ = tmem + 128, tW1 = tmem + 384;   // U, two DZ buffers, dW1
+  const int ksteps = a.e / 16;
+  bool ok = true;
+  int i = 0, p = 0;
+  if (first) {
+    const uint64_t dW1 = sdesc_k128(smem_u32(m.w1)), dW2 = sdesc_mn128(smem_u32(m.w2), d * 128);
+    const uint64_t dE = sdesc_k128(smem_u32(m.e)), dY = sdesc_k128(smem_u32(m.y));
+    constexpr uint32_t id_u = idesc_bf16(128, 128), id_z = idesc_bf16(128, 128, true, false);
+    RingPos y;
+    for (int t = 0; t < a.plan.T && ok; ++t) {
+      int lo, hi;
+      if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+      ok = mbar_wait(&m.bars[WB_W], p & 1);
+      ++p;
+      for (int at = lo; at < hi; at += 128, ++i) {
+        const int b = i & 1;
+        ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);
+        if (i > 0) ok = ok && mbar_wait(&m.bars[WB_UFREE], (i - 1) & 1);   // U read into registers
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t de = desc_add(dE, b * cfg.e_bytes);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ksteps)
+            mma_ss(tU, desc_add(dW1, (k >> 2) * 16384 + (k & 3) * 32), desc_add(de, (k >> 2) * 16384 + (k & 3) * 32), id_u,
+                   k ? 1u : 0u);
+        mma_commit(&m.bars[WB_UFULL]);
+        if (i >= 2) ok = mbar_wait(&m.bars[WB_USED + b], ((i >> 1) & 1) ^ 1);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          ok = ok && mbar_wait(&m.bars[WB_YFULL + y.s], y.ph);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dy = desc_add(dY, y.s * 16384);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tZ + b * 128, desc_add(dW2, c * 8192 + k * 2048), desc_add(dy, k * 32), id_z, (c | k) ? 1u : 0u);
+          mma_commit(&m.bars[WB_YEMPTY + y.s]);
+          y.next(cfg.units1);
+        }
+        if (!ok) break;
+        mma_commit(&m.bars[WB_ZFULL + b]);
+      }
+    }
+    return;
+  }
+  const uint64_t dEm = sdesc_mn128(smem_u32(m.e), 16384);
+  const uint32_t id_1 = idesc_bf16(128, a.e, false, true);
+  for (int t = 0; t < a.plan.T && ok; ++t) {
+    int lo, hi;
+    if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+    if (p > 0) ok = mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1);
+    ++p;
+    for (int at = lo; at < hi; at += 128, ++i) {
+      const int b = i & 1;
+      ok = ok && mbar_wait(&m.bars[WB_READY + b], (i >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t de = desc_add(dEm, b * cfg.e_bytes);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {      // 16 slots: hi in 8 columns, lo in the next 8
+        const uint32_t du = tZ + b * 128 + k * 16;
+        mma_ts(tW1, du, desc_add(de, k * 2048), id_1, at > lo || k ? 1u : 0u);
+        mma_ts(tW1, du + 8, desc_add(de, k * 2048), id_1, 1u);
+      }
+      mma_commit(&m.bars[WB_USED + b]);
+      mma_commit(&m.bars[WB_EEMPTY + b]);
+    }
+    mma_commit(&m.bars[WB_ACCFULL]);
+  }
+}
+
+// Role 2's products; U buffers beside dW2: two up to d = 256, else one.
+template <int NC>
+__device__ inline void wg_products2(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, uint32_t tmem, int tile0,
+                                    int tile1, bool first) {
+  constexpr int d = NC * 64, NBU = d <= 256 ? 2 : 1;
+  const uint32_t tW2 = tmem, tU = tmem + (NBU == 2 ? 256 : 384);
+  const int ksteps = a.e / 16;
+  bool ok = true;
+  int i = 0, p = 0;
+  RingPos u;                       // U buffer of the step
+  if (first) {
+    const uint64_t dW1 = sdesc_k128(smem_u32(m.w1)), dE = sdesc_k128(smem_u32(m.e));
+    constexpr uint32_t id_u = idesc_bf16(128, 128);
+    for (int t = 0; t < a.plan.T && ok; ++t) {
+      int lo, hi;
+      if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+      ok = mbar_wait(&m.bars[WB_W], p & 1);
+      ++p;
+      for (int at = lo; at < hi; at += 128, ++i) {
+        const int b = i & 1;
+        ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);
+        if (i >= NBU) ok = ok && mbar_wait(&m.bars[WB_USED + u.s], u.ph ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t de = desc_add(dE, b * cfg.e_bytes);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ksteps)
+            mma_ss(tU + u.s * 128, desc_add(dW1, (k >> 2) * 16384 + (k & 3) * 32),
+                   desc_add(de, (k >> 2) * 16384 + (k & 3) * 32), id_u, k ? 1u : 0u);
+        mma_commit(&m.bars[WB_UFULL + u.s]);
+        mma_commit(&m.bars[WB_EEMPTY + b]);
+        u.next(NBU);
+      }
+    }
+    return;
+  }
+  const uint64_t dY = sdesc_mn128(smem_u32(m.y), 8192);
+  constexpr int n0 = d > 256 ? 256 : d, n1 = d - n0;
+  constexpr uint32_t id_2 = idesc_bf16(128, n0, false, true), id_2b = idesc_bf16(128, n1 ? n1 : 16, false, true);
+  RingPos y;
+  for (int t = 0; t < a.plan.T && ok; ++t) {
+    int lo, hi;
+    if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+    if (p > 0) ok = mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1);
+    ++p;
+    for (int at = lo; at < hi; at += 128, ++i) {
+      ok = ok && mbar_wait(&m.bars[WB_READY + u.s], u.ph);
+      if (!ok) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ok = ok && mbar_wait(&m.bars[WB_YFULL + y.s], y.ph);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t dy = desc_add(dY, y.s * (d * 128));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t z = tU + u.s * 128 + h * 64 + k * 16;
+          mma_ts(tW2, z, desc_add(dy, k * 2048), id_2, at > lo || h || k ? 1u : 0u);
+          mma_ts(tW2, z + 8, desc_add(dy, k * 2048), id_2, 1u);
+          if (n1) {
+            mma_ts(tW2 + n0, z, desc_add(dy, n0 * 128 + k * 2048), id_2b, at > lo || h || k ? 1u : 0u);
+            mma_ts(tW2 + n0, z + 8, desc_add(dy, n0 * 128 + k * 2048), id_2b, 1u);
+          }
+        }
+        mma_commit(&m.bars[WB_YEMPTY + y.s]);
+        y.next(cfg.units2);
+      }
+      mma_commit(&m.bars[WB_USED + u.s]);
+      u.next(NBU);
+    }
+    mma_commit(&m.bars[WB_ACCFULL]);
+  }
+}
+
+// The lane's partial sums of 32 slots added over the warp's 32 lanes: lane l
+// returns slot l's total (halving exchanges, 31 shuffles).
+__device__ inline float reduce_slots(float* v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float give = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
+      v[j] = keep + __shfl_xor_sync(~0u, give, o);
+    }
+  }
+  return v[0];
+}
+
+template <int NC, bool DOT>
+__device__ inline void wg_compute1(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, const WgArgs& w,
+                                   uint32_t tmem, int tile0, int tile1, int chunk, int slice) {
+  constexpr int d = NC * 64;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q4 = warp & 3, sg = warp >> 2;         // hidden quarter, 32 of the step's slots
+  const int h = chunk * 128 + q4 * 32 + lane;
+  const bool real = chunk * 128 + q4 * 32 < d;     // the same for the warp: d is a multiple of 64
+  const uint32_t lb = ((uint32_t)(q4 * 32) << 16) + sg * 32;
+  const uint32_t tU = tmem + lb, tZ = tmem + 128 + lb, tW1 = tmem + 384 + ((uint32_t)(q4 * 32) << 16);
+  bool ok = true;
+  int i = 0, p = 0;
+  for (int t = 0; t < a.plan.T; ++t) {
+    int lo, hi;
+    if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+    const float b1s = real ? __bfloat162float(((const __nv_bfloat16*)a.mlp.b1[t])[h]) : 0.f;
+    const uint64_t b1 = f2_pack(b1s, b1s);
+    uint64_t db1 = f2_pack(0.f, 0.f);
+#pragma unroll 1
+    for (int at = lo; at < hi; at += 128, ++i) {
+      const int b = i & 1;
+      ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);   // the choice weights
+      ok = ok && mbar_wait(&m.bars[WB_UFULL], i & 1);
+      tc_fence_after();
+      const float* wt = m.wt + b * 128 + sg * 32;
+      uint64_t g[16], z[DOT ? 16 : 1];             // w GELU'(u), GELU(u)
+      {
+        float v[32];
+        tmem_ld32(tU, v);
+        tc_fence_before();
+        warp_arrive(&m.bars[WB_UFREE]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const GeluPair r = gelu_pair(f2_add(f2_pack(v[2 * j], v[2 * j + 1]), b1));
+          const float2 wj = *(const float2*)(wt + 2 * j);
+          g[j] = f2_mul(gelu_slope(r), f2_pack(wj.x, wj.y));
+          if (DOT) z[j] = r.z;
+        }
+      }
+      ok = ok && mbar_wait(&m.bars[WB_ZFULL + b], (i >> 1) & 1);
+      tc_fence_after();
+      uint32_t rows[16];                           // du of slots 2j, 2j + 1, rounded
+      float dot[DOT ? 32 : 1];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float y[16];
+        tmem_ld16(tZ + b * 128 + hf * 16, y);
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t dz = f2_pack(y[2 * j], y[2 * j + 1]);
+          if (DOT) f2_unpack(f2_mul(dz, z[hf * 8 + j]), dot[hf * 16 + 2 * j], dot[hf * 16 + 2 * j + 1]);
+          const uint64_t du = f2_mul(dz, g[hf * 8 + j]);
+          db1 = f2_add(db1, du);
+          split_pair(du, pk[j], pk[8 + j]);
+          rows[hf * 8 + j] = pk[j];
+        }
+        tmem_st16(tZ + b * 128 + hf * 16, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&m.bars[WB_READY + b]);
+      if (w.du && real) {
+        // two lanes exchange halves, so that each stores two neighbouring
+        // units of one slot: the even lane slot 2j, the odd one slot 2j + 1
+        __nv_bfloat16* o = w.du + (long long)(at + sg * 32 + (lane & 1)) * d + (h & ~1);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t other = __shfl_xor_sync(~0u, rows[j], 1);
+          *(uint32_t*)(o + (long long)j * 2 * d) =
+              lane & 1 ? __byte_perm(other, rows[j], 0x7632) : __byte_perm(rows[j], other, 0x5410);
+        }
+      }
+      if (DOT) {
+        const float s = reduce_slots(dot);
+        w.dot[(long long)(at + sg * 32 + lane) * (cfg.chunks * 4) + chunk * 4 + q4] = s;
+      }
+    }
+    ok = ok && mbar_wait(&m.bars[WB_ACCFULL], p & 1);
+    tc_fence_after();
+    float* out = piece_at(w.p1, slice, t);
+    for (int c0 = sg * 16; c0 < a.e; c0 += 64) {
+      float v[16];
+      tmem_ld16(tW1 + c0, v);
+      if (real && ok) {
+        float4* o = (float4*)(out + (long long)h * a.e + c0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+    }
+    tc_fence_before();
+    // db1: the four slot groups, through W1's tile (its products are done, and
+    // the next weights wait for the accumulators to be free)
+    float* red = (float*)m.w1;
+    float x, y;
+    f2_unpack(db1, x, y);
+    red[sg * 128 + q4 * 32 + lane] = x + y;
+    asm volatile("bar.sync 2, 512;" ::: "memory");
+    if (sg == 0 && real && ok) {
+      const float* r = red + q4 * 32 + lane;
+      out[(long long)d * a.e + h] = (r[0] + r[128]) + (r[256] + r[384]);
+    }
+    asm volatile("bar.sync 2, 512;" ::: "memory");
+    fence_async_smem();            // the weights that follow are written by TMA
+    warp_arrive(&m.bars[WB_ACCFREE]);
+    ++p;
+  }
+}
+
+template <int NC>
+__device__ inline void wg_compute2(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, const WgArgs& w,
+                                   uint32_t tmem, int tile0, int tile1, int chunk, int slice) {
+  constexpr int d = NC * 64, NBU = d <= 256 ? 2 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q4 = warp & 3, sg = warp >> 2;
+  const int h0 = chunk * 128, h = h0 + q4 * 32 + lane;
+  const bool real = h0 + q4 * 32 < d;
+  const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+  const uint32_t tW2 = tmem + lane_base, tU = tmem + (NBU == 2 ? 256 : 384) + lane_base + sg * 32;
+  const int oc = h0 / 8 + (threadIdx.x & 15), og = threadIdx.x >> 4;   // db2: 8 output columns, 2 slots of a unit
+  bool ok = true;
+  int i = 0, p = 0;
+  RingPos u, yr;
+  for (int t = 0; t < a.plan.T; ++t) {
+    int lo, hi;
+    if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+    const float b1s = real ? __bfloat162float(((const __nv_bfloat16*)a.mlp.b1[t])[h]) : 0.f;
+    const uint64_t b1 = f2_pack(b1s, b1s);
+    float db2[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int at = lo; at < hi; at += 128, ++i) {
+      const int b = i & 1;
+      ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);   // the choice weights
+      ok = ok && mbar_wait(&m.bars[WB_UFULL + u.s], u.ph);
+      tc_fence_after();
+      const float* wt = m.wt + b * 128;
+      const uint32_t from = tU + u.s * 128;
+      {
+        float v[32];
+        tmem_ld32(from, v);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int n = hf * 16 + 2 * j;
+            const GeluPair r = gelu_pair(f2_add(f2_pack(v[n], v[n + 1]), b1));
+            const float2 wj = *(const float2*)(wt + sg * 32 + n);
+            split_pair(f2_mul(r.z, f2_pack(wj.x, wj.y)), pk[j], pk[8 + j]);
+          }
+          tmem_st16(from + hf * 16, pk);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&m.bars[WB_READY + u.s]);
+      u.next(NBU);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {             // db2 from the DY units, before they are freed
+        ok = ok && mbar_wait(&m.bars[WB_YFULL + yr.s], yr.ph);
+        if (oc * 8 < d) {
+          const uint8_t* box = m.y + yr.s * (d * 128) + (oc >> 3) * 8192;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = og * 2 + j;
+            const uint4 x = *(const uint4*)(box + r * 128 + (((oc & 7) ^ (r & 7)) << 4));
+            const __nv_bfloat162* xh = (const __nv_bfloat162*)&x;
+            const float wr = wt[hf * 64 + r];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const float2 f = __bfloat1622float2(xh[n]);
+              db2[2 * n] = fmaf(wr, f.x, db2[2 * n]);
+              db2[2 * n + 1] = fmaf(wr, f.y, db2[2 * n + 1]);
+            }
+          }
+        }
+        warp_arrive(&m.bars[WB_YEMPTY + yr.s]);
+        yr.next(cfg.units2);
+      }
+      warp_arrive(&m.bars[WB_EEMPTY + b]);         // the choice weights have been used
+    }
+    // the piece's sums: dW2 [o][h] with neighbouring lanes on neighbouring h
+    ok = ok && mbar_wait(&m.bars[WB_ACCFULL], p & 1);
+    tc_fence_after();
+    float* out = piece_at(w.p2, slice, t);
+    for (int c0 = sg * 32; c0 < d; c0 += 128) {
+      float v[32];
+      tmem_ld32(tW2 + c0, v);
+      if (real && ok)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) out[(long long)(c0 + j) * d + h] = v[j];
+    }
+    tc_fence_before();
+    float* red = (float*)m.w1;     // [32][128]
+#pragma unroll
+    for (int n = 0; n < 8; ++n) red[og * 128 + (threadIdx.x & 15) * 8 + n] = db2[n];
+    asm volatile("bar.sync 2, 512;" ::: "memory");
+    if (threadIdx.x < 128 && h0 + threadIdx.x < d && ok) {
+      float sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < 32; ++n) sum += red[n * 128 + threadIdx.x];
+      out[(long long)d * d + h0 + threadIdx.x] = sum;
+    }
+    asm volatile("bar.sync 2, 512;" ::: "memory");
+    fence_async_smem();
+    warp_arrive(&m.bars[WB_ACCFREE]);
+    ++p;
+  }
+}
+
+template <int NC, bool DOT>
+__global__ void __launch_bounds__(kWgThreads, 1)
+    routed_wgrad_kernel(const __grid_constant__ RoutedMaps maps, const RoutedTcArgs a, const WgArgs w) {
+  constexpr int d = NC * 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const WgCfg cfg = wg_cfg(a.e, d);
+  WgShared m;
+  m.w1 = smem;
+  m.e = m.w1 + cfg.w1_bytes;
+  m.w2 = m.e + 2 * cfg.e_bytes;
+  m.off = (long long*)(m.w2 + cfg.ring);
+  m.row = (int*)(m.off + 256);
+  m.wt = (float*)(m.row + 256);
+  m.bars = (uint64_t*)(m.wt + 256);
+  m.spans = (PlanSpans*)(m.bars + WB_SPANS);
+  if (smem_u32(smem) & 1023) {
+    if (threadIdx.x == 0) flag_error(kErrSmemAlign);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // role 1 takes the first CTAs: chunk after chunk of every slice
+  const int n1 = cfg.chunks * w.p1.slices;
+  const bool role1 = (int)blockIdx.x < n1;
+  const int id = role1 ? blockIdx.x : blockIdx.x - n1;
+  const int chunk = id % cfg.chunks, slice = id / cfg.chunks;
+  m.y = role1 ? m.w2 + d * 256 : m.w2;
+  uint32_t* tmem_slot = (uint32_t*)(m.bars + WB_TMEM);
+  if (threadIdx.x == 0) {
+    auto init = [&](int bar, int n, int count) {
+      for (int i = 0; i < n; ++i) mbar_init(&m.bars[bar + i], count);
+    };
+    init(WB_EFULL, 2, 4);
+    init(WB_EEMPTY, 2, role1 ? 1 : 1 + kWgCompute);
+    init(WB_YFULL, 8, 4);
+    init(WB_YEMPTY, 8, role1 ? 1 : 1 + kWgCompute);
+    init(WB_UFULL, 2, 1);
+    init(WB_UFREE, 2, kWgCompute);
+    init(WB_ZFULL, 2, 1);
+    init(WB_READY, 2, kWgCompute);
+    init(WB_USED, 2, 1);
+    init(WB_W, 1, 1);
+    init(WB_ACCFULL, 1, 1);
+    init(WB_ACCFREE, 1, kWgCompute);
+    fence_barrier_init();
+  }
+  if (warp == 21) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_launch();
+  load_spans(a.plan, m.spans);
+  const WeightPieces& wp = role1 ? w.p1 : w.p2;
+  const int tile0 = slice * wp.per, tile1 = min(tile0 + wp.per, m.spans->first[a.plan.T] / 128);
+
+  if (warp >= 21) {
+    if (role1) wg_products1<NC>(a, cfg, m, tmem, tile0, tile1, warp == 21);
+    else wg_products2<NC>(a, cfg, m, tmem, tile0, tile1, warp == 21);
+  } else if (warp == 20) {
+    if (lane == 0) {
+      const uint64_t keep = l2_evict_last();
+      int p = 0;
+      for (int t = 0; t < a.plan.T; ++t) {
+        int lo, hi;
+        if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+        // the last piece's products are done when its sums have been taken out
+        if (p > 0 && !mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1)) break;
+        ++p;
+        uint64_t* full = &m.bars[WB_W];
+        mbar_expect_tx(full, cfg.w1_bytes + (role1 ? d * 256 : 0));
+        for (int b = 0; b < cfg.eb; ++b)
+          for (int j = 0; j < 2; ++j)
+            tma_load_3d_hint(&maps.w1[t], full, m.w1 + b * 16384 + j * 8192, b * 64, chunk * 128 + j * 64, 0, keep);
+        for (int j = 0; role1 && j < 2; ++j)
+          for (int b = 0; b < NC; ++b)
+            tma_load_3d_hint(&maps.w2[t], full, m.w2 + j * d * 128 + b * 8192, chunk * 128 + j * 64, b * 64, 0, keep);
+      }
+    }
+  } else if (warp >= kWgCompute) {
+    if (role1) wg_gather<NC, true>(a, cfg, m, tile0, tile1);
+    else wg_gather<NC, false>(a, cfg, m, tile0, tile1);
+  } else {
+    if (role1) wg_compute1<NC, DOT>(a, cfg, m, w, tmem, tile0, tile1, chunk, slice);
+    else wg_compute2<NC>(a, cfg, m, w, tmem, tile0, tile1, chunk, slice);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 21) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------ event gradient --
+// DE = du W1 (M = 128 slots, N = e, K = d) from the rows of du that the
+// weight-gradient kernel left, tile by tile; out to the events' rows (k = 1)
+// or to part.  Bound by reading du (2 d bytes a slot, most of it still in L2).
+// Warps 0-3 output, 4-7 load du, 8 loads weights, 9 products.
+constexpr int kDevThreads = 320;
+
+struct DevCfg {
+  int w_bytes, units, smem;                      // W1 of one behaviour, ring of [128 slots x 64] boxes
+};
 __host__ __device__ inline DevCfg dev_cfg(int e, int d) {
   DevCfg c;
-  const int eb = (e + 63) / 64;
-  c.a_bytes = d * 256 + eb * 16384;              // dtoken rows, then event rows
-  c.w1_bytes = eb * 8192;
-  const int fixed = 512 + 512 + 1024 + 512;      // barriers and spans, dw partials, row offsets and indices
-  const int bias = 4 * d * 4;
-  const int room = kSmemMax - fixed - bias - kDevW1 * c.w1_bytes;
-  c.abuf = room >= 2 * c.a_bytes + 4 * 8192 ? 2 : 1;
-  c.units = (room - c.abuf * c.a_bytes) / 8192;
-  if (c.units > 12) c.units = 12;
-  c.smem = fixed + bias + c.abuf * c.a_bytes + kDevW1 * c.w1_bytes + c.units * 8192;
+  c.w_bytes = (e + 63) / 64 * d * 128;
+  c.units = (kSmemMax - 1024 - c.w_bytes) / 16384;
+  if (c.units > 8) c.units = 8;
+  c.smem = 1024 + c.w_bytes + c.units * 16384;
   return c;
 }
 
 template <int NC>
-__global__ void __launch_bounds__(kTokThreads, 1)
-    routed_devents_kernel(const __grid_constant__ RoutedMaps maps, const RoutedTcArgs a) {
+__global__ void __launch_bounds__(kDevThreads, 1)
+    routed_devents_kernel(const __grid_constant__ RoutedMaps maps, const RoutedTcArgs a, const __nv_bfloat16* __restrict__ du) {
   constexpr int d = NC * 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   const DevCfg cfg = dev_cfg(a.e, d);
-  uint8_t* sA = smem;
-  uint8_t* sW1 = sA + cfg.abuf * cfg.a_bytes;
-  uint8_t* sW2 = sW1 + kDevW1 * cfg.w1_bytes;
-  float* sBias = (float*)(sW2 + cfg.units * 8192);   // [2][2 d]
-  long long* sOff = (long long*)(sBias + 4 * d);     // [128]
-  int* sRow = (int*)(sOff + 128);                    // [128]
-  float* sDot = (float*)(sRow + 128);                // [128]
-  uint64_t* bars = (uint64_t*)(sDot + 128);
-  uint64_t* a_full = bars;           // [2]
-  uint64_t* a_empty = bars + 2;      // [2]
-  uint64_t* w1_full = bars + 4;      // [2]
-  uint64_t* w1_empty = bars + 6;     // [2]
-  uint64_t* w2_full = bars + 8;      // [12]
-  uint64_t* w2_empty = bars + 20;    // [12]
-  uint64_t* u_full = bars + 32;      // [2]
-  uint64_t* du_ready = bars + 34;    // [2]
-  uint64_t* du_done = bars + 36;     // [2]
-  uint64_t* de_full = bars + 38;     // [2]
-  uint64_t* de_empty = bars + 40;    // [2]
-  uint64_t* b_free = bars + 42;      // [2]
-  uint64_t* b_full = bars + 44;      // [2]
-  uint32_t* tmem_slot = (uint32_t*)(bars + 46);
-  PlanSpans* spans = (PlanSpans*)(bars + 48);
-
+  uint8_t* sW = smem;
+  uint8_t* sA = sW + cfg.w_bytes;
+  uint64_t* bars = (uint64_t*)(sA + cfg.units * 16384);
+  uint64_t* a_full = bars;           // [8]
+  uint64_t* a_empty = bars + 8;      // [8]
+  uint64_t* e_full = bars + 16;      // [2]
+  uint64_t* e_empty = bars + 18;     // [2]
+  uint64_t* w_full = bars + 20;
+  uint64_t* w_empty = bars + 21;
+  uint32_t* tmem_slot = (uint32_t*)(bars + 22);
+  PlanSpans* spans = (PlanSpans*)(bars + 24);
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) flag_error(kErrSmemAlign);
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], 4);
-      mbar_init(&a_empty[i], 1 + kTokGelu);
-      mbar_init(&w1_full[i], 1);
-      mbar_init(&w1_empty[i], 1);
-      mbar_init(&u_full[i], 1);
-      mbar_init(&du_ready[i], kTokGelu);
-      mbar_init(&du_done[i], 1);
-      mbar_init(&de_full[i], 1);
-      mbar_init(&de_empty[i], kTokOut);
-      mbar_init(&b_full[i], 4);
-      mbar_init(&b_free[i], kTokGelu);
-    }
     for (int i = 0; i < cfg.units; ++i) {
-      mbar_init(&w2_full[i], 1);
-      mbar_init(&w2_empty[i], 1);
+      mbar_init(&a_full[i], 4);
+      mbar_init(&a_empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&e_full[i], 1);
+      mbar_init(&e_empty[i], 4);
+    }
+    mbar_init(w_full, 1);
+    mbar_init(w_empty, 1);
     fence_barrier_init();
   }
-  if (warp == 17) tmem_alloc(tmem_slot, 512);
+  if (warp == 9) tmem_alloc(tmem_slot, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tE = tmem, tU = tmem + 256, tZ = tmem + 384;   // two buffers each of DE (128), U, DZ (64 columns)
   grid_dep_wait();
   grid_dep_launch();
   const bool fine = load_spans(a.plan, spans);
   const int T = a.plan.T, n_tiles = spans->first[T] / 128;
-  const int step = gridDim.x;
+  // neighbouring tiles to one CTA: its weights change only between behaviours
+  const int per = (n_tiles + gridDim.x - 1) / gridDim.x;
+  const int t0 = blockIdx.x * per, t1 = min(t0 + per, n_tiles);
 
-  if (warp == 16) {
-    // ------------------------------------------------------ weight producer
+  if (warp == 8) {
     if (lane == 0) {
       const uint64_t keep = l2_evict_last();
-      RingPos w1, w2;
-      bool wrap1 = false, wrap2 = false, ok = true;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += step) {
+      int prev = -1, p = 0;
+      for (int tile = t0; tile < t1; ++tile) {
         const int t = span_type(spans, T, tile * 128);
-        for (int c = 0; c < NC && ok; ++c) {
-          ok = !wrap1 || mbar_wait(&w1_empty[w1.s], w1.ph ^ 1);
-          if (!ok) break;
-          uint8_t* to = sW1 + w1.s * cfg.w1_bytes;
-          mbar_expect_tx(&w1_full[w1.s], cfg.w1_bytes);
-          tma_load_3d_hint(&maps.w1[t], &w1_full[w1.s], to, 0, c * 64, 0, keep);
-          if (cfg.w1_bytes > 8192) tma_load_3d_hint(&maps.w1[t], &w1_full[w1.s], to + 8192, 64, c * 64, 0, keep);
-          w1.next(kDevW1);
-          wrap1 = wrap1 || w1.s == 0;
-          for (int b = 0; b < NC; ++b) {
-            ok = !wrap2 || mbar_wait(&w2_empty[w2.s], w2.ph ^ 1);
-            if (!ok) break;
-            mbar_expect_tx(&w2_full[w2.s], 8192);
-            tma_load_3d_hint(&maps.w2[t], &w2_full[w2.s], sW2 + w2.s * 8192, c * 64, b * 64, 0, keep);
-            w2.next(cfg.units);
-            wrap2 = wrap2 || w2.s == 0;
-          }
-        }
+        if (t == prev) continue;
+        if (p > 0 && !mbar_wait(w_empty, (p - 1) & 1)) break;
+        prev = t;
+        ++p;
+        mbar_expect_tx(w_full, cfg.w_bytes);
+        for (int b = 0; b * 64 < a.e; ++b)
+          for (int c = 0; c < NC; ++c)
+            tma_load_3d_hint(&maps.w1[t], w_full, sW + b * (d * 128) + c * 8192, b * 64, c * 64, 0, keep);
       }
     }
-  } else if (warp == 17) {
-    // ------------------------------------------------------------- products
-    {
-      const uint64_t dA = sdesc_k128(smem_u32(sA)), dW1 = sdesc_k128(smem_u32(sW1));
-      const uint64_t dW1t = sdesc_mn128(smem_u32(sW1), 8192), dW2t = sdesc_mn128(smem_u32(sW2), 8192);
-      constexpr uint32_t id_u = idesc_bf16(128, 64), id_z = idesc_bf16(128, 64, false, true);
-      const uint32_t id_e = idesc_bf16(128, a.e, false, true);
-      const int ksteps = a.e / 16;
-      const int mine = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - (int)blockIdx.x) / step + 1 : 0;
-      const int total = mine * NC;
-      bool ok = true;
-      RingPos ar, w1u, w1d, w2;
-      int gu = 0, cu = 0, cd = 0, i = 0;
-      auto up = [&]() {
-        ok = ok && mbar_wait(&w1_full[w1u.s], w1u.ph);
-        if (cu == 0) ok = ok && mbar_wait(&a_full[ar.s], ar.ph);
-        if (gu >= 2) ok = ok && mbar_wait(&du_done[gu & 1], ((gu >> 1) & 1) ^ 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t da = desc_add(dA, ar.s * cfg.a_bytes), dw = desc_add(dW1, w1u.s * cfg.w1_bytes);
-        const uint32_t u = tU + (gu & 1) * 64, z = tZ + (gu & 1) * 64;
+  } else if (warp == 9) {
+    const uint64_t dA = sdesc_k128(smem_u32(sA)), dW = sdesc_mn128(smem_u32(sW), d * 128);
+    const uint32_t id_e = idesc_bf16(128, a.e, false, true);
+    bool ok = true;
+    RingPos r;
+    int prev = -1, p = 0, i = 0;
+    for (int tile = t0; tile < t1 && ok; ++tile, ++i) {
+      const int t = span_type(spans, T, tile * 128);
+      if (t != prev) {
+        if (p > 0) mma_commit(w_empty);      // the last behaviour's products
+        ok = mbar_wait(w_full, p & 1);
+        prev = t;
+        ++p;
+      }
+      if (i >= 2) ok = ok && mbar_wait(&e_empty[i & 1], ((i >> 1) & 1) ^ 1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < ksteps)
-            mma_ss(u, desc_add(da, d * 256 + (k >> 2) * 16384 + (k & 3) * 32),
-                      desc_add(dw, (k >> 2) * 8192 + (k & 3) * 32), id_u, k ? 1u : 0u);
-#pragma unroll
-        for (int b = 0; b < NC; ++b) {       // 64 of the contraction per W2 unit
-          ok = mbar_wait(&w2_full[w2.s], w2.ph);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t dz = desc_add(dW2t, w2.s * 8192);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(z, desc_add(da, b * 16384 + k * 32), desc_add(dz, k * 2048), id_z, (b | k) ? 1u : 0u);
-          mma_commit(&w2_empty[w2.s]);
-          w2.next(cfg.units);
-        }
-        mma_commit(&u_full[gu & 1]);
-        if (++cu == NC) {
-          cu = 0;
-          mma_commit(&a_empty[ar.s]);
-          ar.next(cfg.abuf);
-        }
-        w1u.next(kDevW1);
-        ++gu;
-      };
-      if (total > 0) up();
-      for (int g = 0; g < total && ok; ++g) {
-        // the next chunk's products run during this chunk's GELU; a new
-        // tile's only after this one's last, since its rows may still be coming
-        const bool same = cd + 1 < NC;
-        if (same) up();
-        ok = ok && mbar_wait(&du_ready[g & 1], (g >> 1) & 1);
-        if (cd == 0 && i >= 2) ok = ok && mbar_wait(&de_empty[i & 1], ((i >> 1) & 1) ^ 1);
+      for (int c = 0; c < NC; ++c) {
+        ok = ok && mbar_wait(&a_full[r.s], r.ph);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t w1 = desc_add(dW1t, w1d.s * cfg.w1_bytes);
-        const uint32_t to = tE + (i & 1) * 128;
+        const uint64_t da = desc_add(dA, r.s * 16384);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t du = tU + (g & 1) * 64 + k * 16;   // hi in 8 columns, lo in the next 8
-          mma_ts(to, du, desc_add(w1, k * 2048), id_e, (cd | k) ? 1u : 0u);
-          mma_ts(to, du + 8, desc_add(w1, k * 2048), id_e, 1u);
-        }
-        mma_commit(&w1_empty[w1d.s]);
-        mma_commit(&du_done[g & 1]);
-        w1d.next(kDevW1);
-        if (++cd == NC) {
-          cd = 0;
-          mma_commit(&de_full[i & 1]);
-          ++i;
-        }
-        if (!same && g + 1 < total) up();
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + (i & 1) * 128, desc_add(da, k * 32), desc_add(dW, c * 8192 + k * 2048), id_e, (c | k) ? 1u : 0u);
+        mma_commit(&a_empty[r.s]);
+        r.next(cfg.units);
       }
+      mma_commit(&e_full[i & 1]);
     }
-  } else if (warp >= 12) {
-    // --------------------------------------------------------------- gather
-    const int tid = threadIdx.x - 12 * 32;
-    bool ok = true;
-    RingPos ar;
-    int i = 0;
-    int flat = (int)blockIdx.x < n_tiles ? a.plan.order[(long long)blockIdx.x * 128 + tid] : -1;
-    for (int tile = blockIdx.x; tile < n_tiles; tile += step, ++i) {
-      const int row = flat < 0 ? -1 : flat / a.plan.k;
-      if (tile + step < n_tiles) flat = a.plan.order[(long long)(tile + step) * 128 + tid];
-      if (i >= cfg.abuf) ok = ok && mbar_wait(&a_empty[ar.s], ar.ph ^ 1);
-      uint8_t* at = sA + ar.s * cfg.a_bytes;
-      sOff[tid] = row < 0 ? -1LL : token_off(a.rows, row, d);
-      sRow[tid] = row;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (ok) {
-        gather_boxes<128, NC>(at, [&](int r) { return sOff[r]; }, 128, d, a.dtokens, tid);
-        gather_events<128>(at + d * 256, sRow, 128, a.e, a.events, tid);
-      }
-      if (i >= 2) ok = ok && mbar_wait(&b_free[i & 1], ((i >> 1) & 1) ^ 1);
-      load_biases(sBias + (i & 1) * 2 * d, a.mlp, span_type(spans, T, tile * 128), d, tid, 128);
-      warp_arrive(&b_full[i & 1]);
-      cp_async_commit();
-      cp_async_wait<0>();
+  } else if (warp >= 4) {
+    // two boxes' copies stay in flight while a third is issued
+    const int tid = threadIdx.x - 128;
+    bool ok = true, wrapped = false;
+    int pending = 0;
+    RingPos r, f;
+    auto arrive = [&]() {
       fence_async_smem();
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      warp_arrive(&a_full[ar.s]);
-      ar.next(cfg.abuf);
-    }
+      warp_arrive(&a_full[f.s]);
+      f.next(cfg.units);
+      --pending;
+    };
+    for (int tile = t0; tile < t1; ++tile)
+      for (int c = 0; c < NC; ++c) {
+        if (wrapped) ok = ok && mbar_wait(&a_empty[r.s], r.ph ^ 1);
+        if (ok)
+          gather_boxes<128, 1>(sA + r.s * 16384, [&](int row) { return ((long long)tile * 128 + row) * d + c * 64; }, 128, 64,
+                               du, tid);
+        cp_async_commit();
+        r.next(cfg.units);
+        wrapped = wrapped || r.s == 0;
+        if (++pending == 3) {
+          cp_async_wait<2>();
+          arrive();
+        }
+      }
+    cp_async_wait<0>();
+    while (pending > 0) arrive();
     if (fine && a.devents)
-      zero_unrouted(a.plan, a.devents, TokenRows{0x7fffffff, 0}, a.e, blockIdx.x * 4 + warp - 12, gridDim.x * 4);
-    if (fine && a.dweights) {
-      const long long n = (long long)a.plan.R * a.plan.k;
-      for (long long c = (long long)blockIdx.x * 128 + tid; c < n; c += (long long)gridDim.x * 128)
-        if (a.plan.pos[c] < 0) a.dweights[c] = 0.f;
-    }
-  } else if (warp >= 8) {
-    // --------------------------------------------------------------- output
-    const int q4 = warp & 3;
-    const uint32_t lb = (uint32_t)(q4 * 32) << 16;
+      zero_unrouted(a.plan, a.devents, TokenRows{0x7fffffff, 0}, a.e, blockIdx.x * 4 + warp - 4, gridDim.x * 4);
+  } else {
+    const uint32_t lb = (uint32_t)(warp * 32) << 16;
     bool ok = true;
     int i = 0;
-    for (int tile = blockIdx.x; tile < n_tiles; tile += step, ++i) {
-      const int flat = a.plan.order[(long long)tile * 128 + q4 * 32 + lane];
-      ok = ok && mbar_wait(&de_full[i & 1], (i >> 1) & 1);
+    for (int tile = t0; tile < t1; ++tile, ++i) {
+      const int flat = a.plan.order[(long long)tile * 128 + warp * 32 + lane];
+      ok = ok && mbar_wait(&e_full[i & 1], (i >> 1) & 1);
       tc_fence_after();
-      const uint32_t from = tE + (i & 1) * 128 + lb;
+      const uint32_t from = tmem + (i & 1) * 128 + lb;
       for (int c0 = 0; c0 < a.e; c0 += 16) {
         float v[16];
         tmem_ld16(from + c0, v);
@@ -744,7 +1280,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
           float4* o = (float4*)(a.part + (long long)flat * a.e + c0);
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else if (a.devents) {
+        } else {
           uint4* o = (uint4*)(a.devents + (long long)flat * a.e + c0);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -753,481 +1289,12 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         }
       }
       tc_fence_before();
-      warp_arrive(&de_empty[i & 1]);
-    }
-  } else {
-    // ----------------------------------------------------------------- GELU
-    const int q4 = warp & 3, wq = warp >> 2;
-    const uint32_t lb = ((uint32_t)(q4 * 32) << 16) + wq * 32;
-    const int row = q4 * 32 + lane;
-    bool ok = true;
-    RingPos ar;
-    int i = 0, g = 0;
-    for (int tile = blockIdx.x; tile < n_tiles; tile += step, ++i) {
-      const int flat = a.plan.order[(long long)tile * 128 + row];
-      const float w = flat < 0 ? 0.f : a.weights ? a.weights[flat] : 1.f;
-      const float* bias = sBias + (i & 1) * 2 * d;
-      ok = ok && mbar_wait(&b_full[i & 1], (i >> 1) & 1);
-      float dot = 0.f;
-      if (a.dweights) {       // <dtoken, b2 + emb> over this half of the row's columns
-        ok = ok && mbar_wait(&a_full[ar.s], ar.ph);
-        const uint8_t* at = sA + ar.s * cfg.a_bytes + row * 128;
-#pragma unroll 4
-        for (int c = wq * NC * 4; c < (wq + 1) * NC * 4; ++c) {
-          const uint4 x = *(const uint4*)(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
-          const float4 s0 = *(const float4*)(bias + d + c * 8), s1 = *(const float4*)(bias + d + c * 8 + 4);
-          const __nv_bfloat162* xh = (const __nv_bfloat162*)&x;
-          const float2 p0 = __bfloat1622float2(xh[0]), p1 = __bfloat1622float2(xh[1]);
-          const float2 p2 = __bfloat1622float2(xh[2]), p3 = __bfloat1622float2(xh[3]);
-          dot = fmaf(p0.x, s0.x, fmaf(p0.y, s0.y, fmaf(p1.x, s0.z, fmaf(p1.y, s0.w, dot))));
-          dot = fmaf(p2.x, s1.x, fmaf(p2.y, s1.y, fmaf(p3.x, s1.z, fmaf(p3.y, s1.w, dot))));
-        }
-      }
-      warp_arrive(&a_empty[ar.s]);
-      ar.next(cfg.abuf);
-#pragma unroll 1
-      for (int c = 0; c < NC; ++c, ++g) {
-        ok = ok && mbar_wait(&u_full[g & 1], (g >> 1) & 1);
-        tc_fence_after();
-        const uint32_t u = tU + (g & 1) * 64 + lb, z = tZ + (g & 1) * 64 + lb;
-        const float* b1 = bias + c * 64 + wq * 32;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {       // 16 units: 8 columns of hi, 8 of lo
-          float v[16], y[16];
-          tmem_ld16(u + h * 16, v);
-          tmem_ld16(z + h * 16, y);
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 b = *(const float2*)(b1 + h * 16 + 2 * j);
-            float z0, g0, z1, g1;
-            gelu_and_slope_fast(v[2 * j] + b.x, z0, g0);
-            gelu_and_slope_fast(v[2 * j + 1] + b.y, z1, g1);
-            dot = fmaf(y[2 * j], z0, dot);
-            dot = fmaf(y[2 * j + 1], z1, dot);
-            split_bf16x2(w * y[2 * j] * g0, w * y[2 * j + 1] * g1, pk[j], pk[8 + j]);
-          }
-          tmem_st16(u + h * 16, pk);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&du_ready[g & 1]);
-      }
-      warp_arrive(&b_free[i & 1]);
-      if (a.dweights) {
-        if (wq == 1) sDot[row] = dot;
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (wq == 0 && flat >= 0 && ok) a.dweights[flat] = dot + sDot[row];
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-      }
+      warp_arrive(&e_empty[i & 1]);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) tmem_dealloc(tmem, 512);
-}
-
-// ----------------------------------------------------------- weight gradients --
-// A CTA holds 128 hidden units of one behaviour at a time and walks its slice
-// of the slots, 64 per step, transposed so that hidden units are TMEM lanes:
-//   U^T = W1c E^T (M = 128, N = 64, K = e), DZ^T = W2c^T DY^T (K = d);
-//   z, du by eight warps, each split into two bf16 terms over the columns it
-//   came from, which makes them A operands where they are:
-//   dW2c^T [128][d] += z DY, dW1c [128][e] += du E (K = 64 slots).
-// So the hidden rows are recomputed but never stored, db1 is a sum inside a
-// thread, and the gathered rows serve as both K-major and MN-major operands.
-// With d > 256 dW2c^T takes 384 TMEM columns and leaves no room for the rest:
-// two CTAs share a hidden chunk, one with U, DZ and dW1c, one with U and dW2c
-// (about the same number of tensor-core cycles each).
-// u(i + 1) is issued once dW2(i) has read z, and GELU(i + 1) then runs during
-// dW1(i) and dz(i + 1).
-// Warps 0-7 compute, 8-11 gather, 12 loads weights, 13 issues the products.
-constexpr int kWgThreads = 448, kWgCompute = 8;
-
-struct WgCfg {
-  int eb, chunks, roles, stages;   // hidden chunks of 128, CTAs per slice, row stages
-  int w1_bytes, w2_bytes, stage_bytes, smem;
-};
-__host__ __device__ inline WgCfg wg_cfg(int e, int d) {
-  WgCfg c;
-  c.eb = (e + 63) / 64;
-  c.chunks = (d + 127) / 128;
-  c.roles = d > 256 ? 2 * c.chunks : c.chunks;
-  c.w1_bytes = c.eb * 16384;
-  c.w2_bytes = 2 * d * 128;
-  c.stage_bytes = d * 128 + c.eb * 8192;
-  // barriers and spans, row offsets and indices of two steps; a stage also
-  // holds its 64 choice weights
-  const int fixed = 512 + 2 * 64 * 12;
-  c.stages = (kSmemMax - fixed - c.w1_bytes - c.w2_bytes) / (c.stage_bytes + 256);
-  if (c.stages > 4) c.stages = 4;
-  c.smem = fixed + c.w1_bytes + c.w2_bytes + c.stages * (c.stage_bytes + 256);
-  return c;
-}
-
-template <int NC>
-__global__ void __launch_bounds__(kWgThreads, 1)
-    routed_wgrad_kernel(const __grid_constant__ RoutedMaps maps, const RoutedTcArgs a, const WeightPieces w) {
-  constexpr int d = NC * 64;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const WgCfg cfg = wg_cfg(a.e, d);
-  uint8_t* sW1 = smem;
-  uint8_t* sW2 = sW1 + cfg.w1_bytes;
-  uint8_t* sS = sW2 + cfg.w2_bytes;
-  float* sWt = (float*)(sS + cfg.stages * cfg.stage_bytes);    // [stages][64] choice weights
-  long long* sOff = (long long*)(sWt + cfg.stages * 64);       // [2][64] dtoken rows of two steps
-  int* sRow = (int*)(sOff + 128);                              // [2][64] event rows
-  uint64_t* bars = (uint64_t*)(sRow + 128);
-  uint64_t* s_full = bars;           // [4]
-  uint64_t* s_empty = bars + 4;      // [4]
-  uint64_t* w_full = bars + 8;
-  uint64_t* u_full = bars + 9;
-  uint64_t* z_ready = bars + 10;
-  uint64_t* z_free = bars + 11;
-  uint64_t* dz_full = bars + 12;
-  uint64_t* du_ready = bars + 13;
-  uint64_t* du_free = bars + 14;
-  uint64_t* acc_full = bars + 15;
-  uint64_t* acc_empty = bars + 16;
-  uint32_t* tmem_slot = (uint32_t*)(bars + 17);
-  PlanSpans* spans = (PlanSpans*)(bars + 18);
-
-  if (smem_u32(smem) & 1023) {
-    if (threadIdx.x == 0) flag_error(kErrSmemAlign);
-    return;
-  }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int role = blockIdx.x % cfg.roles, slice = blockIdx.x / cfg.roles;
-  const int chunk = role % cfg.chunks, h0 = chunk * 128;
-  const bool do1 = role < cfg.chunks;                // DZ, dW1, db1 and db2
-  const bool do2 = d <= 256 || !do1;                 // dW2
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < cfg.stages; ++i) {
-      mbar_init(&s_full[i], 4);
-      mbar_init(&s_empty[i], 1 + kWgCompute);
-    }
-    mbar_init(w_full, 1);
-    mbar_init(u_full, 1);
-    mbar_init(z_ready, kWgCompute);
-    mbar_init(z_free, 1);
-    mbar_init(dz_full, 1);
-    mbar_init(du_ready, kWgCompute);
-    mbar_init(du_free, 1);
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, kWgCompute);
-    fence_barrier_init();
-  }
-  if (warp == 13) tmem_alloc(tmem_slot, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t tW2 = tmem, tW1 = tmem + 256, tU = tmem + 384, tZ = tmem + 448;
-  grid_dep_wait();
-  grid_dep_launch();
-  load_spans(a.plan, spans);
-  const int T = a.plan.T;
-  const int tile0 = slice * w.per, tile1 = min(tile0 + w.per, spans->first[T] / 128);
-  // the slots of behaviour t in this slice: [lo, hi), hi before the padding
-  auto piece = [&](int t, int& lo, int& hi) {
-    lo = max(tile0 * 128, spans->first[t]);
-    hi = min(tile1 * 128, spans->first[t] + spans->cnt[t]);
-    return lo < hi;
-  };
-
-  if (warp == 12) {
-    // ------------------------------------------------------ weight producer
-    if (lane == 0) {
-      const uint64_t keep = l2_evict_last();
-      int p = 0;
-      for (int t = 0; t < T; ++t) {
-        int lo, hi;
-        if (!piece(t, lo, hi)) continue;
-        // the last piece's products are done when its sums have been taken out
-        if (p > 0 && !mbar_wait(acc_empty, (p - 1) & 1)) break;
-        ++p;
-        mbar_expect_tx(w_full, cfg.w1_bytes + (do1 ? cfg.w2_bytes : 0));
-        for (int b = 0; b < cfg.eb; ++b)
-          for (int j = 0; j < 2; ++j)
-            tma_load_3d_hint(&maps.w1[t], w_full, sW1 + b * 16384 + j * 8192, b * 64, h0 + j * 64, 0, keep);
-        for (int j = 0; do1 && j < 2; ++j)
-          for (int b = 0; b < NC; ++b)
-            tma_load_3d_hint(&maps.w2[t], w_full, sW2 + j * d * 128 + b * 8192, h0 + j * 64, b * 64, 0, keep);
-      }
-    }
-  } else if (warp == 13) {
-    // ------------------------------------------------------------- products
-    {
-      const uint64_t dW1 = sdesc_k128(smem_u32(sW1)), dW2 = sdesc_mn128(smem_u32(sW2), d * 128);
-      const uint64_t dSk = sdesc_k128(smem_u32(sS)), dSm = sdesc_mn128(smem_u32(sS), 8192);
-      constexpr uint32_t id_u = idesc_bf16(128, 64), id_z = idesc_bf16(128, 64, true, false);
-      constexpr int n0 = d > 256 ? 256 : d, n1 = d - n0;
-      constexpr uint32_t id_2 = idesc_bf16(128, n0, false, true), id_2b = idesc_bf16(128, n1 ? n1 : 16, false, true);
-      const uint32_t id_1 = idesc_bf16(128, a.e, false, true);
-      const int ksteps = a.e / 16;
-      const bool early = cfg.stages == 1;    // the only row stage is free after dW1 of the step before
-      bool ok = true;
-      int i = 0, p = 0;                      // steps and pieces so far
-      RingPos sn, sg;                        // row stage of the next step, and of the next dW1
-      auto grad1 = [&](int j, bool fresh) {  // dW1 of step j, then its rows are free
-        if (do1) {
-          ok = ok && mbar_wait(du_ready, j & 1);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t rows = desc_add(dSm, sg.s * cfg.stage_bytes + d * 128);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            mma_ts(tW1, tZ + k * 16, desc_add(rows, k * 2048), id_1, fresh && !k ? 0u : 1u);
-            mma_ts(tW1, tZ + k * 16 + 8, desc_add(rows, k * 2048), id_1, 1u);
-          }
-        }
-        mma_commit(du_free);
-        mma_commit(&s_empty[sg.s]);
-        sg.next(cfg.stages);
-      };
-      for (int t = 0; t < T && ok; ++t) {
-        int lo, hi;
-        if (!piece(t, lo, hi)) continue;
-        ok = ok && mbar_wait(w_full, p & 1);
-        if (p > 0) ok = ok && mbar_wait(acc_empty, (p - 1) & 1);
-        const int n = (hi - lo + 63) / 64;
-        for (int q = 0; q < n && ok; ++q, ++i) {
-          if (early && q > 0) grad1(i - 1, q == 1);
-          ok = ok && mbar_wait(&s_full[sn.s], sn.ph);
-          if (i > 0) ok = ok && mbar_wait(z_free, (i - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t rk = desc_add(dSk, sn.s * cfg.stage_bytes), rm = desc_add(dSm, sn.s * cfg.stage_bytes);
-          sn.next(cfg.stages);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < ksteps)
-              mma_ss(tU, desc_add(dW1, (k >> 2) * 16384 + (k & 3) * 32),
-                        desc_add(rk, d * 128 + (k >> 2) * 8192 + (k & 3) * 32), id_u, k ? 1u : 0u);
-          mma_commit(u_full);
-          if (q > 0) {
-            if (!early) grad1(i - 1, q == 1);
-            ok = ok && mbar_wait(du_free, (i - 1) & 1);
-          }
-          if (!ok) break;
-          tc_fence_after();
-          if (do1) {
-#pragma unroll
-            for (int k = 0; k < NC * 4; ++k)
-              mma_ss(tZ, desc_add(dW2, k * 2048), desc_add(rk, (k >> 2) * 8192 + (k & 3) * 32), id_z, k ? 1u : 0u);
-            mma_commit(dz_full);
-          }
-          ok = mbar_wait(z_ready, i & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (do2) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t z = tU + k * 16;
-              mma_ts(tW2, z, desc_add(rm, k * 2048), id_2, q || k ? 1u : 0u);
-              mma_ts(tW2, z + 8, desc_add(rm, k * 2048), id_2, 1u);
-              if (n1) {
-                mma_ts(tW2 + n0, z, desc_add(rm, n0 * 128 + k * 2048), id_2b, q || k ? 1u : 0u);
-                mma_ts(tW2 + n0, z + 8, desc_add(rm, n0 * 128 + k * 2048), id_2b, 1u);
-              }
-            }
-          }
-          mma_commit(z_free);
-        }
-        if (!ok) break;
-        grad1(i - 1, n == 1);
-        ok = ok && mbar_wait(du_free, (i - 1) & 1);
-        mma_commit(acc_full);
-        ++p;
-      }
-    }
-  } else if (warp >= 8) {
-    // --------------------------------------------------------------- gather
-    // With three stages or more a step's copies are in flight while the next
-    // step's are issued, and its arrival follows then.  (With two, the next
-    // step's stage is free only after the products that wait for this arrival.)
-    const bool defer = cfg.stages > 2;
-    const int tid = threadIdx.x - 8 * 32;
-    bool ok = true;
-    int i = 0;
-    RingPos sn, sa;
-    auto arrive = [&]() {
-      fence_async_smem();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      warp_arrive(&s_full[sa.s]);
-      sa.next(cfg.stages);
-    };
-    for (int t = 0; t < T; ++t) {
-      int lo, hi;
-      if (!piece(t, lo, hi)) continue;
-      int flat = tid < 64 && lo + tid < hi ? a.plan.order[lo + tid] : -1;
-      for (int at = lo; at < hi; at += 64, ++i) {
-        const int row = flat < 0 ? -1 : flat / a.plan.k;
-        long long* off = sOff + (i & 1) * 64;
-        int* rows = sRow + (i & 1) * 64;
-        float wt = 0.f;
-        if (tid < 64) {
-          off[tid] = row < 0 ? -1LL : token_off(a.rows, row, d);
-          rows[tid] = row;
-          wt = flat < 0 ? 0.f : a.weights ? a.weights[flat] : 1.f;
-          flat = at + 64 + tid < hi ? a.plan.order[at + 64 + tid] : -1;   // of the next step
-        }
-        if (i >= cfg.stages) ok = ok && mbar_wait(&s_empty[sn.s], sn.ph ^ 1);
-        if (tid < 64) sWt[sn.s * 64 + tid] = wt;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        uint8_t* to = sS + sn.s * cfg.stage_bytes;
-        if (ok) {
-          gather_events<128>(to + d * 128, rows, 64, a.e, a.events, tid);
-          gather_boxes<128, NC>(to, [&](int r) { return off[r]; }, 64, d, a.dtokens, tid);
-        }
-        cp_async_commit();
-        sn.next(cfg.stages);
-        if (!defer) {
-          cp_async_wait<0>();
-          arrive();
-        } else if (i > 0) {
-          cp_async_wait<1>();
-          arrive();
-        }
-      }
-    }
-    if (defer && i > 0) {
-      cp_async_wait<0>();
-      arrive();
-    }
-  } else {
-    // -------------------------------------------------------------- compute
-    const int q4 = warp & 3, wq = warp >> 2;       // hidden quarter, half of the step's slots
-    const uint32_t lb = (uint32_t)(q4 * 32) << 16;
-    const int h = h0 + q4 * 32 + lane;
-    const int oc = threadIdx.x & 15, og = threadIdx.x >> 4;   // db2: 8 columns, 4 slots a step
-    bool ok = true;
-    int i = 0, p = 0;
-    RingPos sn;
-    for (int t = 0; t < T; ++t) {
-      int lo, hi;
-      if (!piece(t, lo, hi)) continue;
-      const float b1 = h < d ? __bfloat162float(((const __nv_bfloat16*)a.mlp.b1[t])[h]) : 0.f;
-      float db1 = 0.f, db2[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int at = lo; at < hi; at += 64, ++i) {
-        ok = ok && mbar_wait(&s_full[sn.s], sn.ph);   // the choice weights
-        const float* wt = sWt + sn.s * 64 + wq * 32;
-        ok = ok && mbar_wait(u_full, i & 1);
-        tc_fence_after();
-        const uint32_t col = lb + wq * 32;
-        float v[32];
-        tmem_ld32(tU + col, v);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int n = hf * 16 + 2 * j;
-            const float2 wj = *(const float2*)(wt + n);
-            float z0, z1, g0, g1;
-            gelu_and_slope_fast(v[n] + b1, z0, g0);
-            gelu_and_slope_fast(v[n + 1] + b1, z1, g1);
-            v[n] = wj.x * g0;
-            v[n + 1] = wj.y * g1;
-            split_bf16x2(wj.x * z0, wj.y * z1, pk[j], pk[8 + j]);
-          }
-          tmem_st16(tU + col + hf * 16, pk);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(z_ready);
-        if (do1) {
-          ok = ok && mbar_wait(dz_full, i & 1);
-          tc_fence_after();
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float y[16];
-            tmem_ld16(tZ + col + hf * 16, y);
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int n = hf * 16 + 2 * j;
-              const float x0 = y[2 * j] * v[n], x1 = y[2 * j + 1] * v[n + 1];
-              db1 += x0 + x1;
-              split_bf16x2(x0, x1, pk[j], pk[8 + j]);
-            }
-            tmem_st16(tZ + col + hf * 16, pk);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          warp_arrive(du_ready);
-          const int c = h0 / 8 + oc;   // db2 of output columns h0 + 8 oc .. + 7
-          if (c * 8 < d) {
-            const uint8_t* box = sS + sn.s * cfg.stage_bytes + (c >> 3) * 8192;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r = og * 4 + j;
-              const uint4 x = *(const uint4*)(box + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-              const __nv_bfloat162* xh = (const __nv_bfloat162*)&x;
-              const float wr = sWt[sn.s * 64 + r];
-#pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                const float2 f = __bfloat1622float2(xh[n]);
-                db2[2 * n] = fmaf(wr, f.x, db2[2 * n]);
-                db2[2 * n + 1] = fmaf(wr, f.y, db2[2 * n + 1]);
-              }
-            }
-          }
-        }
-        warp_arrive(&s_empty[sn.s]);
-        sn.next(cfg.stages);
-      }
-      // the piece's sums: dW2 [o][h] with neighbouring lanes on neighbouring h
-      ok = ok && mbar_wait(acc_full, p & 1);
-      tc_fence_after();
-      float* out = piece_at(w, slice, t);
-      for (int c0 = wq * 32; do2 && c0 < d; c0 += 64) {
-        float v[32];
-        tmem_ld32(tW2 + lb + c0, v);
-        if (h < d && ok)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) out[(long long)(c0 + j) * d + h] = v[j];
-      }
-      if (do1) {
-        for (int c0 = wq * 16; c0 < a.e; c0 += 32) {
-          float v[16];
-          tmem_ld16(tW1 + lb + c0, v);
-          if (h < d && ok) {
-            float4* o = (float4*)(out + (long long)d * d + (long long)h * a.e + c0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          }
-        }
-      }
-      tc_fence_before();
-      if (do1) {
-        // db1: the two halves; db2: the 16 slot groups, through W1's tile (its
-        // products are done, and the next weights wait for acc_empty)
-        float* red = (float*)sW1;    // 128 + 16 x 128 floats
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (wq) red[q4 * 32 + lane] = db1;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) red[128 + og * 128 + oc * 8 + n] = db2[n];
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        float* bias = out + (long long)d * (d + a.e);
-        if (!wq && h < d && ok) bias[h] = db1 + red[q4 * 32 + lane];
-        if (wq && ok) {
-          const int c = threadIdx.x - 128;
-          float sum = 0.f;
-          for (int n = 0; n < 16; ++n) sum += red[128 + n * 128 + c];
-          if (h0 + c < d) bias[d + h0 + c] = sum;
-        }
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        fence_async_smem();          // the weights that follow are written by TMA
-      }
-      warp_arrive(acc_empty);
-      ++p;
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (warp == 9) tmem_dealloc(tmem, 256);
 }
 
 }  // namespace ot
