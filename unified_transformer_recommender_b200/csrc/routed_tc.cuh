@@ -31,8 +31,13 @@ __device__ inline void cp_async16(void* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
                : "memory");
 }
-__device__ inline void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ inline void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Arrives on `bar` when every cp.async that this thread has issued is done (the
+// barrier counts one such arrival per thread).
+__device__ inline void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Shared memory written by threads (cp.async among them) before, seen by
+// tensor-core products and TMA after.
 __device__ inline void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // The product warps run their loops with all 32 lanes and let one elected lane
@@ -106,26 +111,45 @@ __device__ inline int span_type(const PlanSpans* s, int T, int slot) {
   return t;
 }
 
-// Rows of `width` bf16 elements (a multiple of 8, up to 64 NB) into NB boxes
-// of [rows x 64 columns] with the 128-byte swizzle; columns past the width and
-// rows with a negative offset become zero.  off(r): element offset of row r.
-// NT threads; the copies stay in flight.
-template <int NT, int NB, typename Off>
-__device__ inline void gather_boxes(uint8_t* tile, Off off, int rows, int width, const __nv_bfloat16* src, int tid) {
-  for (int i = tid; i < rows * NB * 8; i += NT) {
-    const int r = i / (NB * 8), c = i - r * (NB * 8);   // row, 16-byte chunk
-    const long long o = off(r);
-    const bool on = o >= 0 && c * 8 < width;
-    cp_async16(tile + (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (on ? o + c * 8 : 0), on);
-  }
+// Four warps copy gathered rows into boxes of [rows x 64 columns] with the
+// 128-byte swizzle by cp.async, 16 rows at a time: a thread keeps one 16-byte
+// column of rows r8, r8 + 16, ..., so that the pointers of a tile's rows are
+// set up once for all its boxes and a box is one instruction per row (the
+// gathering warps are otherwise what a step waits for).  No thread waits for
+// its copies: they arrive on the box's barrier by themselves, and the products'
+// warp fences before it reads.
+struct GatherLane {
+  int r8, c, at;                 // first row, 16-byte column, byte offset of it in a box
+  __device__ inline explicit GatherLane(int tid)
+      : r8(tid >> 3), c(tid & 7), at((tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4)) {}
+};
+// ROWS / 16 rows of a box, p[j] + `shift` elements (rows without a source zero).
+template <int ROWS>
+__device__ __forceinline__ void gather_box(const GatherLane& g, uint8_t* box, const __nv_bfloat16* const* p, unsigned on,
+                                           int shift) {
+#pragma unroll
+  for (int j = 0; j < ROWS / 16; ++j) cp_async16(box + g.at + j * 2048, p[j] + (on >> j & 1 ? shift : 0), on >> j & 1);
 }
-// Event rows by index (shared memory, -1: none).
-template <int NT>
-__device__ inline void gather_events(uint8_t* tile, const int* row, int rows, int width, const __nv_bfloat16* src,
-                                     int tid) {
-  auto off = [&](int r) { return (long long)row[r] * width; };
-  if (width <= 64) gather_boxes<NT, 1>(tile, off, rows, width, src, tid);
-  else gather_boxes<NT, 2>(tile, off, rows, width, src, tid);
+// Pointers to rows r8 + 16 j of 128 (row[] in shared memory, -1: none; base
+// stands in for those), at the lane's column.
+__device__ __forceinline__ unsigned gather_rows(const GatherLane& g, const __nv_bfloat16** p, const __nv_bfloat16* base,
+                                                const int* row, int width) {
+  unsigned on = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = row[g.r8 + 16 * j];
+    on |= (r >= 0 ? 1u : 0u) << j;
+    p[j] = r >= 0 ? base + (long long)r * width + g.c * 8 : base;
+  }
+  return on;
+}
+// An event tile of 128 rows: one or two boxes, columns past the width zero.
+__device__ __forceinline__ void gather_events(const GatherLane& g, uint8_t* tile, const __nv_bfloat16* events,
+                                              const int* row, int width) {
+  const __nv_bfloat16* p[8];
+  const unsigned on = gather_rows(g, p, events, row, width);
+  gather_box<128>(g, tile, p, g.c * 8 < width ? on : 0u, 0);
+  if (width > 64) gather_box<128>(g, tile + 16384, p, 64 + g.c * 8 < width ? on : 0u, 64);
 }
 
 // Zero rows for the events without any behaviour (k = 1): a warp looks at 32
@@ -186,7 +210,7 @@ __host__ __device__ inline TokCfg tok_cfg(int e, int d) {
   c.w1_bytes = eb * 8192;
   c.stage_bytes = c.w1_bytes + d * 128;
   // output staging, biases of two tiles, row indices, barriers and spans
-  const int fixed = kTokOut * 32 * 144 + 4 * d * 4 + 128 * 4 + 512;
+  const int fixed = kTokOut * 32 * 144 + 4 * d * 4 + 256 * 4 + 512;
   const int room = kSmemMax - fixed;
   c.ebuf = eb == 1 ? 2 : 1;
   c.slots = (room - c.ebuf * c.e_bytes) / c.stage_bytes;
@@ -207,8 +231,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   uint8_t* sW = sE + cfg.ebuf * cfg.e_bytes;
   uint8_t* sOut = sW + cfg.slots * cfg.stage_bytes;
   float* sBias = (float*)(sOut + kTokOut * 32 * 144);       // [2][2 d]
-  int* sRow = (int*)(sBias + 4 * d);                        // [128]
-  uint64_t* bars = (uint64_t*)(sRow + 128);
+  int* sRow = (int*)(sBias + 4 * d);                        // [2][128]
+  uint64_t* bars = (uint64_t*)(sRow + 256);
   uint64_t* e_full = bars;          // [2]
   uint64_t* e_empty = bars + 2;     // [2]
   uint64_t* w_full = bars + 4;      // [4] a slot's weights
@@ -229,7 +253,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&e_full[i], 4);
+      mbar_init(&e_full[i], 128);
       mbar_init(&e_empty[i], 1);
       mbar_init(&b_full[i], 4);
       mbar_init(&b_free[i], kTokGelu + kTokOut);
@@ -289,7 +313,10 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     for (int tile = blockIdx.x; tile < n_tiles && ok; tile += step) {
       for (int c = 0; c < NC; ++c) {
         ok = mbar_wait(&w_full[r.s], r.ph);      // refilled, so the slot's U is free too
-        if (c == 0) ok = ok && mbar_wait(&e_full[er.s], er.ph);
+        if (c == 0) {
+          ok = ok && mbar_wait(&e_full[er.s], er.ph);
+          fence_async_smem();
+        }
         if (!ok) break;
         tc_fence_after();
         const uint64_t de = desc_add(dE, er.s * cfg.e_bytes), dw = desc_add(dW, r.s * cfg.stage_bytes);
@@ -333,25 +360,23 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   } else if (warp >= 12) {
     // --------------------------------------------------------------- gather
     const int tid = threadIdx.x - 12 * 32;
+    const GatherLane lane_of(tid);
     bool ok = true;
     RingPos e;
     int i = 0;
     int flat = (int)blockIdx.x < n_tiles ? a.plan.order[(long long)blockIdx.x * 128 + tid] : -1;
     for (int tile = blockIdx.x; tile < n_tiles; tile += step, ++i) {
-      if (i >= cfg.ebuf) ok = ok && mbar_wait(&e_empty[e.s], e.ph ^ 1);
-      sRow[tid] = flat < 0 ? -1 : flat / a.plan.k;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (ok) gather_events<128>(sE + e.s * cfg.e_bytes, sRow, 128, a.e, a.events, tid);
+      int* rows = sRow + (i & 1) * 128;
+      rows[tid] = flat < 0 ? -1 : flat / a.plan.k;
       if (tile + step < n_tiles) flat = a.plan.order[(long long)(tile + step) * 128 + tid];
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (i >= cfg.ebuf) ok = ok && mbar_wait(&e_empty[e.s], e.ph ^ 1);
+      if (ok) gather_events(lane_of, sE + e.s * cfg.e_bytes, a.events, rows, a.e);
+      cp_async_arrive(&e_full[e.s]);
+      e.next(cfg.ebuf);
       if (i >= 2) ok = ok && mbar_wait(&b_free[i & 1], ((i >> 1) & 1) ^ 1);
       load_biases(sBias + (i & 1) * 2 * d, a.mlp, span_type(spans, T, tile * 128), d, tid, 128);
       warp_arrive(&b_full[i & 1]);
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_async_smem();
-      asm volatile("bar.sync 1, 128;" ::: "memory");   // sRow free again
-      warp_arrive(&e_full[e.s]);
-      e.next(cfg.ebuf);
     }
     if (!COMBINE && fine) zero_unrouted(a.plan, a.tokens, a.rows, d, blockIdx.x * 4 + warp - 12, gridDim.x * 4);
   } else if (warp >= 8) {
@@ -585,37 +610,15 @@ __device__ inline bool wg_piece(const PlanSpans* s, int tile0, int tile1, int t,
   return lo < hi;
 }
 
-// Gathers the steps' event tiles and DY units.  A load's copies stay in flight
-// while up to depth - 1 newer loads are issued; its arrival follows then.
-// depth is below the ring's size and a step's loads, so that no load waits for
-// a slot that only an arrival still held back could free.
+// Gathers the steps' event tiles and DY units.
 template <int NC, bool ROLE1>
 __device__ inline void wg_gather(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, int tile0, int tile1) {
   constexpr int d = NC * 64;
   const int tid = threadIdx.x - kWgCompute * 32, units = ROLE1 ? cfg.units1 : cfg.units2;
-  const int depth = min(min(3, units - 1), ROLE1 ? NC + 1 : 3);
+  const GatherLane g(tid);
   bool ok = true, wrapped = false;
-  int i = 0, pending = 0, pend0 = 0, pend1 = 0, pend2 = 0;   // barriers of the loads in flight, oldest first
+  int i = 0;
   RingPos y;
-  auto arrive = [&]() {          // the oldest load's copies are done
-    fence_async_smem();
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    warp_arrive(&m.bars[pend0]);
-    pend0 = pend1;
-    pend1 = pend2;
-    --pending;
-  };
-  auto issued = [&](int bar) {
-    cp_async_commit();
-    if (pending == 0) pend0 = bar;
-    else if (pending == 1) pend1 = bar;
-    else pend2 = bar;
-    if (++pending < depth) return;
-    if (depth == 3) cp_async_wait<2>();
-    else if (depth == 2) cp_async_wait<1>();
-    else cp_async_wait<0>();
-    arrive();
-  };
   for (int t = 0; t < a.plan.T; ++t) {
     int lo, hi;
     if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
@@ -630,25 +633,34 @@ __device__ inline void wg_gather(const RoutedTcArgs& a, const WgCfg& cfg, const 
       m.row[b * 128 + tid] = row;
       m.wt[b * 128 + tid] = wt;
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (ok) gather_events<128>(m.e + b * cfg.e_bytes, m.row + b * 128, 128, a.e, a.events, tid);
-      issued(WB_EFULL + b);
-      const long long* off = m.off + b * 128;
+      if (ok) gather_events(g, m.e + b * cfg.e_bytes, a.events, m.row + b * 128, a.e);
+      cp_async_arrive(&m.bars[WB_EFULL + b]);     // also releases the weights written above
+      const __nv_bfloat16* p[8];
+      unsigned on = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const long long o = m.off[b * 128 + g.r8 + 16 * j];
+        on |= (o >= 0 ? 1u : 0u) << j;
+        p[j] = o >= 0 ? a.dtokens + o + g.c * 8 : a.dtokens;
+      }
 #pragma unroll 1
       for (int u = 0; u < (ROLE1 ? NC : 2); ++u) {
         if (wrapped) ok = ok && mbar_wait(&m.bars[WB_YEMPTY + y.s], y.ph ^ 1);
-        if (ok && ROLE1)
-          gather_boxes<128, 1>(m.y + y.s * 16384, [&](int r) { return off[r] < 0 ? -1LL : off[r] + u * 64; }, 128, 64,
-                               a.dtokens, tid);
-        if (ok && !ROLE1)
-          gather_boxes<128, NC>(m.y + y.s * (d * 128), [&](int r) { return off[u * 64 + r]; }, 64, d, a.dtokens, tid);
-        issued(WB_YFULL + y.s);
+        if (ok && ROLE1) gather_box<128>(g, m.y + y.s * 16384, p, on, u * 64);
+        if (ok && !ROLE1) {
+          uint8_t* to = m.y + y.s * (d * 128);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {           // the unit's 64 slots: rows j = 4 u .. 4 u + 3
+            if (u == 0) gather_box<64>(g, to + c * 8192, p, on, c * 64);
+            else gather_box<64>(g, to + c * 8192, p + 4, on >> 4, c * 64);
+          }
+        }
+        cp_async_arrive(&m.bars[WB_YFULL + y.s]);
         y.next(units);
         wrapped = wrapped || y.s == 0;
       }
     }
   }
-  cp_async_wait<0>();
-  while (pending > 0) arrive();
 }
 
 // Role 1's products.
@@ -675,6 +687,7 @@ __device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, con
         ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);
         if (i > 0) ok = ok && mbar_wait(&m.bars[WB_UFREE], (i - 1) & 1);   // U read into registers
         if (!ok) break;
+        fence_async_smem();
         tc_fence_after();
         const uint64_t de = desc_add(dE, b * cfg.e_bytes);
 #pragma unroll
@@ -688,6 +701,7 @@ __device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, con
         for (int c = 0; c < NC; ++c) {
           ok = ok && mbar_wait(&m.bars[WB_YFULL + y.s], y.ph);
           if (!ok) break;
+          fence_async_smem();
           tc_fence_after();
           const uint64_t dy = desc_add(dY, y.s * 16384);
 #pragma unroll
@@ -713,6 +727,7 @@ __device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, con
       const int b = i & 1;
       ok = ok && mbar_wait(&m.bars[WB_READY + b], (i >> 1) & 1);
       if (!ok) break;
+      fence_async_smem();
       tc_fence_after();
       const uint64_t de = desc_add(dEm, b * cfg.e_bytes);
 #pragma unroll
@@ -751,6 +766,7 @@ __device__ inline void wg_products2(const RoutedTcArgs& a, const WgCfg& cfg, con
         ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);
         if (i >= NBU) ok = ok && mbar_wait(&m.bars[WB_USED + u.s], u.ph ^ 1);
         if (!ok) break;
+        fence_async_smem();
         tc_fence_after();
         const uint64_t de = desc_add(dE, b * cfg.e_bytes);
 #pragma unroll
@@ -781,6 +797,7 @@ __device__ inline void wg_products2(const RoutedTcArgs& a, const WgCfg& cfg, con
       for (int h = 0; h < 2; ++h) {
         ok = ok && mbar_wait(&m.bars[WB_YFULL + y.s], y.ph);
         if (!ok) break;
+        fence_async_smem();
         tc_fence_after();
         const uint64_t dy = desc_add(dY, y.s * (d * 128));
 #pragma unroll
@@ -1060,9 +1077,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     auto init = [&](int bar, int n, int count) {
       for (int i = 0; i < n; ++i) mbar_init(&m.bars[bar + i], count);
     };
-    init(WB_EFULL, 2, 4);
+    init(WB_EFULL, 2, 128);
     init(WB_EEMPTY, 2, role1 ? 1 : 1 + kWgCompute);
-    init(WB_YFULL, 8, 4);
+    init(WB_YFULL, 8, 128);
     init(WB_YEMPTY, 8, role1 ? 1 : 1 + kWgCompute);
     init(WB_UFULL, 2, 1);
     init(WB_UFREE, 2, kWgCompute);
@@ -1163,7 +1180,7 @@ __global__ void __launch_bounds__(kDevThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < cfg.units; ++i) {
-      mbar_init(&a_full[i], 4);
+      mbar_init(&a_full[i], 128);
       mbar_init(&a_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1222,6 +1239,7 @@ __global__ void __launch_bounds__(kDevThreads, 1)
       for (int c = 0; c < NC; ++c) {
         ok = ok && mbar_wait(&a_full[r.s], r.ph);
         if (!ok) break;
+        fence_async_smem();
         tc_fence_after();
         const uint64_t da = desc_add(dA, r.s * 16384);
 #pragma unroll
@@ -1233,34 +1251,22 @@ __global__ void __launch_bounds__(kDevThreads, 1)
       mma_commit(&e_full[i & 1]);
     }
   } else if (warp >= 4) {
-    // two boxes' copies stay in flight while a third is issued
-    const int tid = threadIdx.x - 128;
+    const GatherLane g(threadIdx.x - 128);
     bool ok = true, wrapped = false;
-    int pending = 0;
-    RingPos r, f;
-    auto arrive = [&]() {
-      fence_async_smem();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      warp_arrive(&a_full[f.s]);
-      f.next(cfg.units);
-      --pending;
-    };
-    for (int tile = t0; tile < t1; ++tile)
+    RingPos r;
+    for (int tile = t0; tile < t1; ++tile) {
+      const __nv_bfloat16* p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = du + ((long long)tile * 128 + g.r8 + 16 * j) * d + g.c * 8;
+#pragma unroll 1
       for (int c = 0; c < NC; ++c) {
         if (wrapped) ok = ok && mbar_wait(&a_empty[r.s], r.ph ^ 1);
-        if (ok)
-          gather_boxes<128, 1>(sA + r.s * 16384, [&](int row) { return ((long long)tile * 128 + row) * d + c * 64; }, 128, 64,
-                               du, tid);
-        cp_async_commit();
+        if (ok) gather_box<128>(g, sA + r.s * 16384, p, 0xffu, c * 64);
+        cp_async_arrive(&a_full[r.s]);
         r.next(cfg.units);
         wrapped = wrapped || r.s == 0;
-        if (++pending == 3) {
-          cp_async_wait<2>();
-          arrive();
-        }
       }
-    cp_async_wait<0>();
-    while (pending > 0) arrive();
+    }
     if (fine && a.devents)
       zero_unrouted(a.plan, a.devents, TokenRows{0x7fffffff, 0}, a.e, blockIdx.x * 4 + warp - 4, gridDim.x * 4);
   } else {
