@@ -277,9 +277,11 @@ static onetrans_status route_impl(const onetrans_model* m, const int32_t* types,
 template <typename T>
 static onetrans_status combine_launch(const PlanView& plan, const float* part, int width, void* out,
                                       const TokenRows& rows, cudaStream_t st) {
-  const long long items = (long long)plan.R * width;
-  launch_dependent(routed_combine_kernel<T>, dim3((unsigned)std::min<long long>(cdiv(items, 256), 148 * 8)), dim3(256), 0,
-                   st, plan, part, width, (T*)out, rows);
+  const bool wide = width % 8 == 0 && rows.sample_ld % 8 == 0;
+  const long long items = (long long)plan.R * (width / (wide ? 8 : 1));
+  const dim3 grid((unsigned)std::min<long long>(cdiv(items, 256), 148 * 8));
+  if (wide) launch_dependent(routed_combine_kernel<T, 8>, grid, dim3(256), 0, st, plan, part, width, (T*)out, rows);
+  else launch_dependent(routed_combine_kernel<T, 1>, grid, dim3(256), 0, st, plan, part, width, (T*)out, rows);
   return last_launch();
 }
 

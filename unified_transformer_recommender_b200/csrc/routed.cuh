@@ -246,9 +246,9 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
   const T* W2 = (const T*)a.mlp.W2[t];
   constexpr bool B_KMAJOR = STEP == RS_HIDDEN || STEP == RS_HIDDEN_GRAD || STEP == RS_TOKEN;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    float av[4], bv[4];
+  const long long aoff = STEP == RS_DU && aflat >= 0 ? token_off(a.rows, aflat / k, a.d) : 0;
+  float acc[4][4] = {}, av[4], bv[4];
+  auto fetch = [&](int k0) {     // this thread's operands of step k0, into registers
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int kk = k0 + ak + i;
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
         if constexpr (STEP == RS_HIDDEN || STEP == RS_HIDDEN_GRAD)
           v = to_f(((const T*)a.events)[(long long)(aflat / k) * a.e + kk]);
         else if constexpr (STEP == RS_TOKEN) v = a.buf0[(long long)(s0 + ar) * a.d + kk];
-        else if constexpr (STEP == RS_DU) v = operand<T>(((const Td*)a.dtokens)[token_off(a.rows, aflat / k, a.d) + kk]);
+        else if constexpr (STEP == RS_DU) v = operand<T>(((const Td*)a.dtokens)[aoff + kk]);
         else v = a.buf1[(long long)(s0 + ar) * a.d + kk];
       }
       av[i] = v;
@@ -271,6 +271,9 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
       }
       bv[i] = w;
     }
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < K; k0 += 16) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) As[ak + i][ar] = av[i];
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
       *(float4*)&Bs[ty][tx * 4] = make_float4(bv[0], bv[1], bv[2], bv[3]);
     }
     __syncthreads();
+    fetch(k0 + 16);               // in flight over this step's sums (past K: zeros, no access)
 #pragma unroll
     for (int kk = 0; kk < 16; ++kk) {
       const float4 x = *(const float4*)&As[kk][ty * 4], w = *(const float4*)&Bs[kk][tx * 4];
@@ -334,24 +338,56 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
 // ---------------------------------------------------------- shared passes --
 // out[r] = sum over the choices of part[r * k + j] (choices that are none
 // left out), rounded once.  k = 1: the products wrote the rows themselves,
-// and only rows without a behaviour are zeroed here.
-template <typename T>
+// and only rows without a behaviour are zeroed here.  A thread takes V
+// neighbouring columns of a row, the next row's choices behind this one's.
+template <typename T, int V>
 __global__ void __launch_bounds__(256) routed_combine_kernel(PlanView plan, const float* __restrict__ part, int width,
                                                              T* __restrict__ out, TokenRows rows) {
   grid_dep_wait();
   grid_dep_launch();
   if (!plan_ok(plan)) return;
-  const long long items = (long long)plan.R * width;
+  const int per = width / V;
+  const long long items = (long long)plan.R * per;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
-    const int r = (int)(i / width), c = (int)(i - (long long)r * width);
+    const int r = i <= 0x7fffffff ? (int)i / per : (int)(i / per), c = (int)(i - (long long)r * per) * V;
     T* o = out + token_off(rows, r, width) + c;
+    float s[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = 0.f;
     if (plan.k == 1) {
-      if (plan.pos[r] < 0) *o = from_f<T>(0.f);
+      if (plan.pos[r] >= 0) continue;
     } else {
-      float s = 0.f;
-      for (int j = 0; j < plan.k; ++j)
-        if (plan.pos[r * plan.k + j] >= 0) s += part[((long long)r * plan.k + j) * width + c];
-      *o = from_f<T>(s);
+      for (int j0 = 0; j0 < plan.k; j0 += 4) {      // four choices in flight
+        float v[4][V];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const long long f = (long long)r * plan.k + j0 + j;
+          if (j0 + j < plan.k && plan.pos[f] >= 0) {
+            const float* p = part + f * width + c;
+            if constexpr (V == 1) v[j][0] = *p;
+            else
+#pragma unroll
+              for (int e = 0; e < V; e += 4) {
+                const float4 q = *(const float4*)(p + e);
+                v[j][e] = q.x; v[j][e + 1] = q.y; v[j][e + 2] = q.z; v[j][e + 3] = q.w;
+              }
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[j][e] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < V; ++e) s[e] += v[j][e];
+      }
+    }
+    if constexpr (V == 8 && sizeof(T) == 2) {
+      *(uint4*)o = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
+                              pack_bf16x2(s[6], s[7]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = from_f<T>(s[e]);
     }
   }
 }
@@ -419,30 +455,34 @@ __global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, We
     const int lo = max(tile0 * 128, first), hi = min(tile1 * 128, first + plan_count(a.plan, t));
     const int end = min(tile1 * 128, plan_first(a.plan, t + 1));
     if (lo >= end) continue;
-    float acc[4][4] = {}, colsum = 0.f;
-    for (int s = lo; s < hi; s += 16) {
+    float acc[4][4] = {}, colsum = 0.f, av[4], bv[4], wt;
+    auto fetch = [&](int s) {
       const int slot = s + lr, flat = slot < hi ? a.plan.order[slot] : -1;
-      float av[4] = {0.f, 0.f, 0.f, 0.f}, bv[4] = {0.f, 0.f, 0.f, 0.f};
-      float wt = 0.f;
-      if (flat >= 0) {
-        wt = a.weights ? a.weights[flat] : 1.f;
+      wt = flat < 0 ? 0.f : a.weights ? a.weights[flat] : 1.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = m0 + lc + i, c = c0 + lc + i;
-          if (second) {
-            if (m < a.d) av[i] = operand<T>(((const Td*)a.dtokens)[token_off(a.rows, flat / k, a.d) + m]);
-            if (c < a.d) bv[i] = a.buf0[(long long)slot * a.d + c];
-          } else {
-            if (m < a.d) av[i] = a.buf1[(long long)slot * a.d + m];
-            if (c < a.e) bv[i] = to_f(((const T*)a.events)[(long long)(flat / k) * a.e + c]);
-          }
+      for (int i = 0; i < 4; ++i) av[i] = bv[i] = 0.f;
+      if (flat < 0) return;
+      const long long row = second ? token_off(a.rows, flat / k, a.d) : (long long)(flat / k) * a.e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = m0 + lc + i, c = c0 + lc + i;
+        if (second) {
+          if (m < a.d) av[i] = operand<T>(((const Td*)a.dtokens)[row + m]);
+          if (c < a.d) bv[i] = a.buf0[(long long)slot * a.d + c];
+        } else {
+          if (m < a.d) av[i] = a.buf1[(long long)slot * a.d + m];
+          if (c < a.e) bv[i] = to_f(((const T*)a.events)[row + c]);
         }
       }
+    };
+    fetch(lo);
+    for (int s = lo; s < hi; s += 16) {
       __syncthreads();
       *(float4*)&As[lr][lc] = make_float4(av[0], av[1], av[2], av[3]);
       *(float4*)&Bs[lr][lc] = make_float4(bv[0], bv[1], bv[2], bv[3]);
       if (lc == 0) Bs[lr][64] = second ? wt : 1.f;
       __syncthreads();
+      fetch(s + 16);              // in flight over this step's sums
 #pragma unroll
       for (int kk = 0; kk < 16; ++kk) {
         const float4 x = *(const float4*)&As[kk][ty * 4], y = *(const float4*)&Bs[kk][tx * 4];

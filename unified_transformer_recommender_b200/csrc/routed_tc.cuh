@@ -130,26 +130,23 @@ __device__ __forceinline__ void gather_box(const GatherLane& g, uint8_t* box, co
 #pragma unroll
   for (int j = 0; j < ROWS / 16; ++j) cp_async16(box + g.at + j * 2048, p[j] + (on >> j & 1 ? shift : 0), on >> j & 1);
 }
-// Pointers to rows r8 + 16 j of 128 (row[] in shared memory, -1: none; base
-// stands in for those), at the lane's column.
-__device__ __forceinline__ unsigned gather_rows(const GatherLane& g, const __nv_bfloat16** p, const __nv_bfloat16* base,
-                                                const int* row, int width) {
-  unsigned on = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = row[g.r8 + 16 * j];
-    on |= (r >= 0 ? 1u : 0u) << j;
-    p[j] = r >= 0 ? base + (long long)r * width + g.c * 8 : base;
-  }
-  return on;
-}
-// An event tile of 128 rows: one or two boxes, columns past the width zero.
+// An event tile of 128 rows (row[] in shared memory, -1: none) by NT threads:
+// one or two boxes, columns past the width zero.
+template <int NT>
 __device__ __forceinline__ void gather_events(const GatherLane& g, uint8_t* tile, const __nv_bfloat16* events,
                                               const int* row, int width) {
-  const __nv_bfloat16* p[8];
-  const unsigned on = gather_rows(g, p, events, row, width);
-  gather_box<128>(g, tile, p, g.c * 8 < width ? on : 0u, 0);
-  if (width > 64) gather_box<128>(g, tile + 16384, p, 64 + g.c * 8 < width ? on : 0u, 64);
+  constexpr int RS = NT / 8;     // rows at a time: a multiple of 8, so the swizzle is the same for all of a thread's
+#pragma unroll
+  for (int j = 0; j < 128 / RS; ++j) {
+    const int r = row[g.r8 + RS * j];
+    const __nv_bfloat16* p = events + (long long)max(r, 0) * width;
+    const bool on = r >= 0 && g.c * 8 < width;
+    cp_async16(tile + g.at + j * RS * 128, p + (on ? g.c * 8 : 0), on);
+    if (width > 64) {
+      const bool on2 = r >= 0 && 64 + g.c * 8 < width;
+      cp_async16(tile + 16384 + g.at + j * RS * 128, p + (on2 ? 64 + g.c * 8 : 0), on2);
+    }
+  }
 }
 
 // Zero rows for the events without any behaviour (k = 1): a warp looks at 32
@@ -371,7 +368,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       if (tile + step < n_tiles) flat = a.plan.order[(long long)(tile + step) * 128 + tid];
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (i >= cfg.ebuf) ok = ok && mbar_wait(&e_empty[e.s], e.ph ^ 1);
-      if (ok) gather_events(lane_of, sE + e.s * cfg.e_bytes, a.events, rows, a.e);
+      if (ok) gather_events<128>(lane_of, sE + e.s * cfg.e_bytes, a.events, rows, a.e);
       cp_async_arrive(&e_full[e.s]);
       e.next(cfg.ebuf);
       if (i >= 2) ok = ok && mbar_wait(&b_free[i & 1], ((i >> 1) & 1) ^ 1);
@@ -486,10 +483,12 @@ __device__ inline float rcp_ftz(float x) {
 }
 // GELU-tanh and its slope of a pair, to float32 accuracy: with
 // s = 1 / (1 + exp(-2v)), v = c (u + a u^3), GELU(u) = u s and
-// d/du = s + u s (1 - s) (2c + 6 c a u^2)  (0.5 (1 + tanh v) = s).  Two
-// special-function results a value (16 a clock an SM, the bound of these
-// loops), the rest on packed float32 pairs.  |u| large gives s = 0 or 1
-// exactly; u^2 is bounded in the slope, where inf * 0 would follow.
+// d/du = s + u s (1 - s) (2c + 6 c a u^2)  (0.5 (1 + tanh v) = s).  The
+// special-function unit (16 results a clock an SM) bounds these loops, so the
+// two reciprocals of a pair come from one, 1/p = q / (p q); the exponent is
+// held at 2^63 for that (s >= 2^-63 in place of 0: GELU off by |u| 2^-63).
+// The rest runs on packed float32 pairs.  u^2 is bounded in the slope, where
+// inf * 0 would follow for large |u|.
 struct GeluPair {
   uint64_t u2, s, z;
 };
@@ -500,9 +499,10 @@ __device__ __forceinline__ GeluPair gelu_pair(uint64_t u) {
   const uint64_t v = f2_mul(u, f2_fma(r.u2, f2_pack(m2l * c * a, m2l * c * a), f2_pack(m2l * c, m2l * c)));
   float x, y;
   f2_unpack(v, x, y);
-  const uint64_t d = f2_add(f2_pack(ex2_ftz(x), ex2_ftz(y)), f2_pack(1.f, 1.f));
+  const uint64_t d = f2_add(f2_pack(ex2_ftz(fminf(x, 63.f)), ex2_ftz(fminf(y, 63.f))), f2_pack(1.f, 1.f));
   f2_unpack(d, x, y);
-  r.s = f2_pack(rcp_ftz(x), rcp_ftz(y));
+  const float q = rcp_ftz(x * y);
+  r.s = f2_mul(f2_pack(y, x), f2_pack(q, q));
   r.z = f2_mul(u, r.s);
   return r;
 }
@@ -518,7 +518,9 @@ __device__ __forceinline__ void split_pair(uint64_t x, uint32_t& hi, uint32_t& l
   float x0, x1;
   f2_unpack(x, x0, x1);
   hi = pack_bf16x2(x0, x1);
-  lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+  const uint64_t h = f2_pack(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+  f2_unpack(f2_fma(h, f2_pack(-1.f, -1.f), x), x0, x1);
+  lo = pack_bf16x2(x0, x1);
 }
 
 // float32 dtokens rounded to bf16 rows [R][d], the operand type of the
@@ -555,13 +557,18 @@ __global__ void __launch_bounds__(256) routed_round_rows_kernel(const float* __r
 // about 2400 tensor-core cycles a step (d = 256, e = 64) each.
 // Role 1 also writes du, rounded once to bf16, as rows for the event gradient
 // and, where asked, each slot's <dz, z> over its units.
-// Warps 0-15 compute, 16-19 gather, 20 loads weights, 21 first products, 22
-// second products.
-constexpr int kWgThreads = 736, kWgCompute = 16;
+// The bound is the compute warps' two special-function results a value (2048
+// cycles a step) with the rest of their work; their warps run apart by up to a
+// step, so what one waits for overlaps another's arithmetic.
+// Warps 0-15 compute, 16-19 gather DY, 20-21 events (on their own, so that
+// the next step's do not queue behind this step's DY), 22 weights and first
+// products, 23 second products.
+constexpr int kWgThreads = 768, kWgCompute = 16;
 
 struct WgCfg {
   int eb, chunks;                  // event boxes, hidden chunks of 128
   int w1_bytes, e_bytes;
+  int ebuf;                        // event tiles in flight
   int units1, units2;              // DY ring: role 1 [128 slots x 64], role 2 [64 slots x d]
   int ring;                        // bytes behind the event tiles
   int smem;
@@ -572,15 +579,18 @@ __host__ __device__ inline WgCfg wg_cfg(int e, int d) {
   c.chunks = (d + 127) / 128;
   c.w1_bytes = c.eb * 16384;
   c.e_bytes = c.eb * 16384;
-  const int fixed = 512 + 2 * 128 * 16;   // barriers and spans; row offsets, indices and weights of two steps
-  const int room = kSmemMax - fixed - c.w1_bytes - 2 * c.e_bytes;
+  c.ebuf = c.eb == 1 ? 3 : 2;
+  // barriers and spans; dtoken row offsets of two steps, event rows and weights
+  // of ebuf
+  const int fixed = 512 + 2 * 128 * 8 + 3 * 128 * 8;
+  const int room = kSmemMax - fixed - c.w1_bytes - c.ebuf * c.e_bytes;
   c.units1 = (room - d * 256) / 16384;
   if (c.units1 > 8) c.units1 = 8;
   c.units2 = room / (d * 128);
   if (c.units2 > 8) c.units2 = 8;
   const int s1 = d * 256 + c.units1 * 16384, s2 = c.units2 * d * 128;
   c.ring = s1 > s2 ? s1 : s2;
-  c.smem = fixed + c.w1_bytes + 2 * c.e_bytes + c.ring;
+  c.smem = fixed + c.w1_bytes + c.ebuf * c.e_bytes + c.ring;
   return c;
 }
 
@@ -593,14 +603,14 @@ struct WgArgs {
 struct WgShared {                // one CTA's shared memory
   uint8_t *w1, *e, *w2, *y;      // w2: role 1; y: the DY ring
   long long* off;                // [2][128] dtoken rows
-  int* row;                      // [2][128] event rows
-  float* wt;                     // [2][128] choice weights
+  int* row;                      // [ebuf][128] event rows
+  float* wt;                     // [ebuf][128] choice weights
   uint64_t* bars;
   PlanSpans* spans;
 };
 enum : int {   // barriers; pairs and rings by index
-  WB_EFULL = 0, WB_EEMPTY = 2, WB_YFULL = 4, WB_YEMPTY = 12, WB_UFULL = 20, WB_UFREE = 22, WB_ZFULL = 24, WB_READY = 26,
-  WB_USED = 28, WB_W = 30, WB_ACCFULL = 31, WB_ACCFREE = 32, WB_TMEM = 33, WB_SPANS = 34
+  WB_EFULL = 0, WB_EEMPTY = 3, WB_YFULL = 6, WB_YEMPTY = 14, WB_UFULL = 22, WB_UFREE = 24, WB_ZFULL = 26, WB_READY = 28,
+  WB_USED = 30, WB_W = 32, WB_ACCFULL = 33, WB_ACCFREE = 34, WB_TMEM = 35, WB_SPANS = 36
 };
 
 // The slots of behaviour t in tiles [tile0, tile1): [lo, hi), hi before the padding.
@@ -610,7 +620,39 @@ __device__ inline bool wg_piece(const PlanSpans* s, int tile0, int tile1, int t,
   return lo < hi;
 }
 
-// Gathers the steps' event tiles and DY units.
+// Gathers the steps' event tiles and choice weights (two warps).
+__device__ inline void wg_gather_events(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, int tile0, int tile1) {
+  const int tid = threadIdx.x - (kWgCompute + 4) * 32;
+  const GatherLane g(tid);
+  bool ok = true, wrapped = false;
+  RingPos er;
+  for (int t = 0; t < a.plan.T; ++t) {
+    int lo, hi;
+    if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
+    for (int at = lo; at < hi; at += 128) {
+      const int b = er.s;
+      int flat[2];
+      float wt[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) flat[j] = at + j * 64 + tid < hi ? a.plan.order[at + j * 64 + tid] : -1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) wt[j] = flat[j] < 0 ? 0.f : a.weights ? a.weights[flat[j]] : 1.f;
+      if (wrapped) ok = ok && mbar_wait(&m.bars[WB_EEMPTY + b], er.ph ^ 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m.row[b * 128 + j * 64 + tid] = flat[j] < 0 ? -1 : flat[j] / a.plan.k;
+        m.wt[b * 128 + j * 64 + tid] = wt[j];
+      }
+      asm volatile("bar.sync 3, 64;" ::: "memory");
+      if (ok) gather_events<64>(g, m.e + b * cfg.e_bytes, a.events, m.row + b * 128, a.e);
+      cp_async_arrive(&m.bars[WB_EFULL + b]);     // also releases the weights written above
+      er.next(cfg.ebuf);
+      wrapped = wrapped || er.s == 0;
+    }
+  }
+}
+
+// Gathers the steps' DY units (four warps).
 template <int NC, bool ROLE1>
 __device__ inline void wg_gather(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, int tile0, int tile1) {
   constexpr int d = NC * 64;
@@ -625,16 +667,9 @@ __device__ inline void wg_gather(const RoutedTcArgs& a, const WgCfg& cfg, const 
     int flat = lo + tid < hi ? a.plan.order[lo + tid] : -1;
     for (int at = lo; at < hi; at += 128, ++i) {
       const int b = i & 1;
-      const int row = flat < 0 ? -1 : flat / a.plan.k;
-      const float wt = flat < 0 ? 0.f : a.weights ? a.weights[flat] : 1.f;
+      m.off[b * 128 + tid] = flat < 0 ? -1LL : token_off(a.rows, flat / a.plan.k, d);
       flat = at + 128 + tid < hi ? a.plan.order[at + 128 + tid] : -1;   // of the next step
-      if (i >= 2) ok = ok && mbar_wait(&m.bars[WB_EEMPTY + b], ((i >> 1) & 1) ^ 1);
-      m.off[b * 128 + tid] = row < 0 ? -1LL : token_off(a.rows, row, d);
-      m.row[b * 128 + tid] = row;
-      m.wt[b * 128 + tid] = wt;
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (ok) gather_events(g, m.e + b * cfg.e_bytes, a.events, m.row + b * 128, a.e);
-      cp_async_arrive(&m.bars[WB_EFULL + b]);     // also releases the weights written above
       const __nv_bfloat16* p[8];
       unsigned on = 0;
 #pragma unroll
@@ -663,15 +698,37 @@ __device__ inline void wg_gather(const RoutedTcArgs& a, const WgCfg& cfg, const 
   }
 }
 
+// The hidden chunk's weights of behaviour t, when the last piece's sums have
+// been taken out (its products are then done).
+template <int NC, bool ROLE1>
+__device__ inline bool wg_weights(const RoutedMaps& maps, const WgCfg& cfg, const WgShared& m, int t, int chunk, int p) {
+  constexpr int d = NC * 64;
+  if (p > 0 && !mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1)) return false;
+  if ((threadIdx.x & 31) == 0) {
+    const uint64_t keep = l2_evict_last();
+    uint64_t* full = &m.bars[WB_W];
+    mbar_expect_tx(full, cfg.w1_bytes + (ROLE1 ? d * 256 : 0));
+    for (int b = 0; b < cfg.eb; ++b)
+      for (int j = 0; j < 2; ++j)
+        tma_load_3d_hint(&maps.w1[t], full, m.w1 + b * 16384 + j * 8192, b * 64, chunk * 128 + j * 64, 0, keep);
+    for (int j = 0; ROLE1 && j < 2; ++j)
+      for (int b = 0; b < NC; ++b)
+        tma_load_3d_hint(&maps.w2[t], full, m.w2 + j * d * 128 + b * 8192, chunk * 128 + j * 64, b * 64, 0, keep);
+  }
+  __syncwarp();
+  return mbar_wait(&m.bars[WB_W], p & 1);
+}
+
 // Role 1's products.
 template <int NC>
-__device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, uint32_t tmem, int tile0,
+__device__ inline void wg_products1(const RoutedMaps& maps, int chunk, const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, uint32_t tmem, int tile0,
                                     int tile1, bool first) {
   constexpr int d = NC * 64;
   const uint32_t tU = tmem, tZ = tmem + 128, tW1 = tmem + 384;   // U, two DZ buffers, dW1
   const int ksteps = a.e / 16;
   bool ok = true;
   int i = 0, p = 0;
+  RingPos er;
   if (first) {
     const uint64_t dW1 = sdesc_k128(smem_u32(m.w1)), dW2 = sdesc_mn128(smem_u32(m.w2), d * 128);
     const uint64_t dE = sdesc_k128(smem_u32(m.e)), dY = sdesc_k128(smem_u32(m.y));
@@ -680,16 +737,17 @@ __device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, con
     for (int t = 0; t < a.plan.T && ok; ++t) {
       int lo, hi;
       if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
-      ok = mbar_wait(&m.bars[WB_W], p & 1);
+      ok = wg_weights<NC, true>(maps, cfg, m, t, chunk, p);
       ++p;
       for (int at = lo; at < hi; at += 128, ++i) {
         const int b = i & 1;
-        ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);
+        ok = ok && mbar_wait(&m.bars[WB_EFULL + er.s], er.ph);
         if (i > 0) ok = ok && mbar_wait(&m.bars[WB_UFREE], (i - 1) & 1);   // U read into registers
         if (!ok) break;
         fence_async_smem();
         tc_fence_after();
-        const uint64_t de = desc_add(dE, b * cfg.e_bytes);
+        const uint64_t de = desc_add(dE, er.s * cfg.e_bytes);
+        er.next(cfg.ebuf);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < ksteps)
@@ -729,7 +787,7 @@ __device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, con
       if (!ok) break;
       fence_async_smem();
       tc_fence_after();
-      const uint64_t de = desc_add(dEm, b * cfg.e_bytes);
+      const uint64_t de = desc_add(dEm, er.s * cfg.e_bytes);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {      // 16 slots: hi in 8 columns, lo in the next 8
         const uint32_t du = tZ + b * 128 + k * 16;
@@ -737,7 +795,8 @@ __device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, con
         mma_ts(tW1, du + 8, desc_add(de, k * 2048), id_1, 1u);
       }
       mma_commit(&m.bars[WB_USED + b]);
-      mma_commit(&m.bars[WB_EEMPTY + b]);
+      mma_commit(&m.bars[WB_EEMPTY + er.s]);
+      er.next(cfg.ebuf);
     }
     mma_commit(&m.bars[WB_ACCFULL]);
   }
@@ -745,37 +804,37 @@ __device__ inline void wg_products1(const RoutedTcArgs& a, const WgCfg& cfg, con
 
 // Role 2's products; U buffers beside dW2: two up to d = 256, else one.
 template <int NC>
-__device__ inline void wg_products2(const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, uint32_t tmem, int tile0,
+__device__ inline void wg_products2(const RoutedMaps& maps, int chunk, const RoutedTcArgs& a, const WgCfg& cfg, const WgShared& m, uint32_t tmem, int tile0,
                                     int tile1, bool first) {
   constexpr int d = NC * 64, NBU = d <= 256 ? 2 : 1;
   const uint32_t tW2 = tmem, tU = tmem + (NBU == 2 ? 256 : 384);
   const int ksteps = a.e / 16;
   bool ok = true;
   int i = 0, p = 0;
-  RingPos u;                       // U buffer of the step
+  RingPos u, er;                   // U buffer and event tile of the step
   if (first) {
     const uint64_t dW1 = sdesc_k128(smem_u32(m.w1)), dE = sdesc_k128(smem_u32(m.e));
     constexpr uint32_t id_u = idesc_bf16(128, 128);
     for (int t = 0; t < a.plan.T && ok; ++t) {
       int lo, hi;
       if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
-      ok = mbar_wait(&m.bars[WB_W], p & 1);
+      ok = wg_weights<NC, false>(maps, cfg, m, t, chunk, p);
       ++p;
       for (int at = lo; at < hi; at += 128, ++i) {
-        const int b = i & 1;
-        ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);
+        ok = ok && mbar_wait(&m.bars[WB_EFULL + er.s], er.ph);
         if (i >= NBU) ok = ok && mbar_wait(&m.bars[WB_USED + u.s], u.ph ^ 1);
         if (!ok) break;
         fence_async_smem();
         tc_fence_after();
-        const uint64_t de = desc_add(dE, b * cfg.e_bytes);
+        const uint64_t de = desc_add(dE, er.s * cfg.e_bytes);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < ksteps)
             mma_ss(tU + u.s * 128, desc_add(dW1, (k >> 2) * 16384 + (k & 3) * 32),
                    desc_add(de, (k >> 2) * 16384 + (k & 3) * 32), id_u, k ? 1u : 0u);
         mma_commit(&m.bars[WB_UFULL + u.s]);
-        mma_commit(&m.bars[WB_EEMPTY + b]);
+        mma_commit(&m.bars[WB_EEMPTY + er.s]);
+        er.next(cfg.ebuf);
         u.next(NBU);
       }
     }
@@ -848,6 +907,7 @@ __device__ inline void wg_compute1(const RoutedTcArgs& a, const WgCfg& cfg, cons
   const uint32_t tU = tmem + lb, tZ = tmem + 128 + lb, tW1 = tmem + 384 + ((uint32_t)(q4 * 32) << 16);
   bool ok = true;
   int i = 0, p = 0;
+  RingPos er;
   for (int t = 0; t < a.plan.T; ++t) {
     int lo, hi;
     if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
@@ -857,10 +917,11 @@ __device__ inline void wg_compute1(const RoutedTcArgs& a, const WgCfg& cfg, cons
 #pragma unroll 1
     for (int at = lo; at < hi; at += 128, ++i) {
       const int b = i & 1;
-      ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);   // the choice weights
+      ok = ok && mbar_wait(&m.bars[WB_EFULL + er.s], er.ph);   // the choice weights
       ok = ok && mbar_wait(&m.bars[WB_UFULL], i & 1);
       tc_fence_after();
-      const float* wt = m.wt + b * 128 + sg * 32;
+      const float* wt = m.wt + er.s * 128 + sg * 32;
+      er.next(cfg.ebuf);
       uint64_t g[16], z[DOT ? 16 : 1];             // w GELU'(u), GELU(u)
       {
         float v[32];
@@ -901,6 +962,7 @@ __device__ inline void wg_compute1(const RoutedTcArgs& a, const WgCfg& cfg, cons
       if (w.du && real) {
         // two lanes exchange halves, so that each stores two neighbouring
         // units of one slot: the even lane slot 2j, the odd one slot 2j + 1
+        // (unit by unit, 16 bytes a lane, took twice as long: a line a lane)
         __nv_bfloat16* o = w.du + (long long)(at + sg * 32 + (lane & 1)) * d + (h & ~1);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -951,14 +1013,14 @@ __device__ inline void wg_compute2(const RoutedTcArgs& a, const WgCfg& cfg, cons
   constexpr int d = NC * 64, NBU = d <= 256 ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q4 = warp & 3, sg = warp >> 2;
-  const int h0 = chunk * 128, h = h0 + q4 * 32 + lane;
-  const bool real = h0 + q4 * 32 < d;
+  const int h = chunk * 128 + q4 * 32 + lane;
+  const bool real = chunk * 128 + q4 * 32 < d;
   const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
   const uint32_t tW2 = tmem + lane_base, tU = tmem + (NBU == 2 ? 256 : 384) + lane_base + sg * 32;
-  const int oc = h0 / 8 + (threadIdx.x & 15), og = threadIdx.x >> 4;   // db2: 8 output columns, 2 slots of a unit
   bool ok = true;
   int i = 0, p = 0;
-  RingPos u, yr;
+  const int oc = chunk * 16 + (threadIdx.x & 15), og = threadIdx.x >> 4;   // db2: 8 output columns, 2 slots of a unit
+  RingPos u, er, yr;
   for (int t = 0; t < a.plan.T; ++t) {
     int lo, hi;
     if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
@@ -967,11 +1029,10 @@ __device__ inline void wg_compute2(const RoutedTcArgs& a, const WgCfg& cfg, cons
     float db2[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int at = lo; at < hi; at += 128, ++i) {
-      const int b = i & 1;
-      ok = ok && mbar_wait(&m.bars[WB_EFULL + b], (i >> 1) & 1);   // the choice weights
+      ok = ok && mbar_wait(&m.bars[WB_EFULL + er.s], er.ph);   // the choice weights
       ok = ok && mbar_wait(&m.bars[WB_UFULL + u.s], u.ph);
       tc_fence_after();
-      const float* wt = m.wt + b * 128;
+      const float* wt = m.wt + er.s * 128;
       const uint32_t from = tU + u.s * 128;
       {
         float v[32];
@@ -1015,7 +1076,8 @@ __device__ inline void wg_compute2(const RoutedTcArgs& a, const WgCfg& cfg, cons
         warp_arrive(&m.bars[WB_YEMPTY + yr.s]);
         yr.next(cfg.units2);
       }
-      warp_arrive(&m.bars[WB_EEMPTY + b]);         // the choice weights have been used
+      warp_arrive(&m.bars[WB_EEMPTY + er.s]);      // the choice weights have been used
+      er.next(cfg.ebuf);
     }
     // the piece's sums: dW2 [o][h] with neighbouring lanes on neighbouring h
     ok = ok && mbar_wait(&m.bars[WB_ACCFULL], p & 1);
@@ -1029,15 +1091,15 @@ __device__ inline void wg_compute2(const RoutedTcArgs& a, const WgCfg& cfg, cons
         for (int j = 0; j < 32; ++j) out[(long long)(c0 + j) * d + h] = v[j];
     }
     tc_fence_before();
-    float* red = (float*)m.w1;     // [32][128]
+    float* red = (float*)m.w1;     // [32][128]; W1's products are done, the next weights wait for ACCFREE
 #pragma unroll
     for (int n = 0; n < 8; ++n) red[og * 128 + (threadIdx.x & 15) * 8 + n] = db2[n];
     asm volatile("bar.sync 2, 512;" ::: "memory");
-    if (threadIdx.x < 128 && h0 + threadIdx.x < d && ok) {
+    if (threadIdx.x < 128 && chunk * 128 + threadIdx.x < d && ok) {
       float sum = 0.f;
 #pragma unroll
       for (int n = 0; n < 32; ++n) sum += red[n * 128 + threadIdx.x];
-      out[(long long)d * d + h0 + threadIdx.x] = sum;
+      out[(long long)d * d + chunk * 128 + threadIdx.x] = sum;
     }
     asm volatile("bar.sync 2, 512;" ::: "memory");
     fence_async_smem();
@@ -1055,17 +1117,17 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   WgShared m;
   m.w1 = smem;
   m.e = m.w1 + cfg.w1_bytes;
-  m.w2 = m.e + 2 * cfg.e_bytes;
+  m.w2 = m.e + cfg.ebuf * cfg.e_bytes;
   m.off = (long long*)(m.w2 + cfg.ring);
   m.row = (int*)(m.off + 256);
-  m.wt = (float*)(m.row + 256);
-  m.bars = (uint64_t*)(m.wt + 256);
+  m.wt = (float*)(m.row + 3 * 128);
+  m.bars = (uint64_t*)(m.wt + 3 * 128);
   m.spans = (PlanSpans*)(m.bars + WB_SPANS);
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) flag_error(kErrSmemAlign);
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   // role 1 takes the first CTAs: chunk after chunk of every slice
   const int n1 = cfg.chunks * w.p1.slices;
   const bool role1 = (int)blockIdx.x < n1;
@@ -1077,8 +1139,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     auto init = [&](int bar, int n, int count) {
       for (int i = 0; i < n; ++i) mbar_init(&m.bars[bar + i], count);
     };
-    init(WB_EFULL, 2, 128);
-    init(WB_EEMPTY, 2, role1 ? 1 : 1 + kWgCompute);
+    init(WB_EFULL, 3, 64);
+    init(WB_EEMPTY, 3, role1 ? 1 : 1 + kWgCompute);
     init(WB_YFULL, 8, 128);
     init(WB_YEMPTY, 8, role1 ? 1 : 1 + kWgCompute);
     init(WB_UFULL, 2, 1);
@@ -1091,7 +1153,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     init(WB_ACCFREE, 1, kWgCompute);
     fence_barrier_init();
   }
-  if (warp == 21) tmem_alloc(tmem_slot, 512);
+  if (warp == 22) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1102,29 +1164,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   const WeightPieces& wp = role1 ? w.p1 : w.p2;
   const int tile0 = slice * wp.per, tile1 = min(tile0 + wp.per, m.spans->first[a.plan.T] / 128);
 
-  if (warp >= 21) {
-    if (role1) wg_products1<NC>(a, cfg, m, tmem, tile0, tile1, warp == 21);
-    else wg_products2<NC>(a, cfg, m, tmem, tile0, tile1, warp == 21);
-  } else if (warp == 20) {
-    if (lane == 0) {
-      const uint64_t keep = l2_evict_last();
-      int p = 0;
-      for (int t = 0; t < a.plan.T; ++t) {
-        int lo, hi;
-        if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
-        // the last piece's products are done when its sums have been taken out
-        if (p > 0 && !mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1)) break;
-        ++p;
-        uint64_t* full = &m.bars[WB_W];
-        mbar_expect_tx(full, cfg.w1_bytes + (role1 ? d * 256 : 0));
-        for (int b = 0; b < cfg.eb; ++b)
-          for (int j = 0; j < 2; ++j)
-            tma_load_3d_hint(&maps.w1[t], full, m.w1 + b * 16384 + j * 8192, b * 64, chunk * 128 + j * 64, 0, keep);
-        for (int j = 0; role1 && j < 2; ++j)
-          for (int b = 0; b < NC; ++b)
-            tma_load_3d_hint(&maps.w2[t], full, m.w2 + j * d * 128 + b * 8192, chunk * 128 + j * 64, b * 64, 0, keep);
-      }
-    }
+  if (warp >= 22) {
+    if (role1) wg_products1<NC>(maps, chunk, a, cfg, m, tmem, tile0, tile1, warp == 22);
+    else wg_products2<NC>(maps, chunk, a, cfg, m, tmem, tile0, tile1, warp == 22);
+  } else if (warp >= kWgCompute + 4) {
+    wg_gather_events(a, cfg, m, tile0, tile1);
   } else if (warp >= kWgCompute) {
     if (role1) wg_gather<NC, true>(a, cfg, m, tile0, tile1);
     else wg_gather<NC, false>(a, cfg, m, tile0, tile1);
@@ -1134,7 +1178,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 21) tmem_dealloc(tmem, 512);
+  if (warp == 22) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------ event gradient --
