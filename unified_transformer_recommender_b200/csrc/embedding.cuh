@@ -82,10 +82,33 @@ __device__ inline uint32_t emb_key(Id id, uint32_t n_rows) {
 // ----------------------------------------------------------------- lookup --
 constexpr int kLookThreads = 256;
 
+// N consecutive elements as they are in memory, 16 bytes at most per access.
+template <typename T, int N> struct EmbRaw {
+  static constexpr int W = N * (int)sizeof(T) / 4;      // words (a lone bf16: half of one)
+  uint32_t w[W ? W : 1];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (W == 0) w[0] = *(const unsigned short*)p;
+    else if constexpr (W == 1) w[0] = *(const uint32_t*)p;
+    else if constexpr (W == 2) { const uint2 q = *(const uint2*)p; w[0] = q.x; w[1] = q.y; }
+    else
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 q = *(const uint4*)(p + i * 4 / (int)sizeof(T));
+        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+      }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    else return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+  }
+};
+
 // A thread keeps its group of VE columns (cpr of them a row, at most
-// kLookThreads) and walks U rows: the ids of all of them are loaded before the
-// first row, so that U row reads are in flight per thread.  Wider rows go
-// over in blocks of kLookThreads groups (blockIdx.y).
+// kLookThreads; wider rows go over in blocks, blockIdx.y) and walks rows, U at
+// a time: U row reads are in flight, as read, and with them the ids of the
+// next U rows, so that only the first ids are waited for.  (One CTA per U rows
+// waited for ids and rows in turn: 29 us against the floor's 14 for 524288
+// rows of 64 bf16.)
 template <typename Tt, typename To, typename Id, int VE, int U>
 __global__ void __launch_bounds__(kLookThreads) emb_lookup_kernel(const Tt* __restrict__ table, uint32_t n_rows,
                                                                   int width, const Id* __restrict__ ids, long long R,
@@ -93,30 +116,37 @@ __global__ void __launch_bounds__(kLookThreads) emb_lookup_kernel(const Tt* __re
                                                                   long long out_ld) {
   const int rpb = kLookThreads / cpr, r = threadIdx.x / cpr;   // rows a CTA looks at together
   const int col = (blockIdx.y * kLookThreads + threadIdx.x - r * cpr) * VE;
-  const long long r0 = (long long)blockIdx.x * rpb * U + r;
+  const long long step = (long long)gridDim.x * rpb * U;
   grid_dep_wait();
   grid_dep_launch();
   if (r >= rpb || col >= width) return;
-  uint32_t key[U];
+  long long r0 = (long long)blockIdx.x * rpb * U + r;
+  Id id[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) key[u] = r0 + u * rpb < R ? emb_key(ids[r0 + u * rpb], n_rows) : n_rows;
-  float v[U][VE];
+  for (int u = 0; u < U; ++u) id[u] = r0 + u * rpb < R ? ids[r0 + u * rpb] : (Id)-1;
+  for (; r0 < R; r0 += step) {
+    EmbRaw<Tt, VE> v[U];
+    unsigned on = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (key[u] < n_rows) {
-      emb_ld<VE>(table + (long long)key[u] * width + col, v[u]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VE; ++e) v[u][e] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      const uint32_t key = emb_key(id[u], n_rows);
+      if (key < n_rows) {
+        v[u].load(table + (long long)key * width + col);
+        on |= 1u << u;
+      }
     }
-  }
-  To* o = out + r0 * out_ld + col;
+    const long long next = r0 + step;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (r0 + u * rpb < R) {
+    for (int u = 0; u < U; ++u) id[u] = next + u * rpb < R ? ids[next + u * rpb] : (Id)-1;
+    To* o = out + r0 * out_ld + col;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) v[u][e] *= key[u] < n_rows ? scale : 0.f;
-      emb_st<VE>(o + (long long)u * rpb * out_ld, v[u]);
+    for (int u = 0; u < U; ++u) {
+      if (r0 + u * rpb < R) {
+        float x[VE];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[e] = on >> u & 1 ? v[u].get(e) * scale : 0.f;
+        emb_st<VE>(o + (long long)u * rpb * out_ld, x);
+      }
     }
   }
 }

@@ -24,19 +24,19 @@ static onetrans_status lookup_impl(const void* table, long long n_rows, int widt
   int ve = sizeof(Tt) == 4 && sizeof(To) == 4 ? 4 : 8;
   while (width % ve || out_ld % ve) ve >>= 1;
   const int groups = width / ve, cpr = std::min(groups, kLookThreads), rpb = kLookThreads / cpr;
-  // eight rows in flight per thread once that still gives every SM two CTAs
-  const bool many = R >= 2LL * 148 * 8 * rpb;
-  const dim3 grid((unsigned)cdiv(R, rpb * (many ? 8 : 1)), (unsigned)cdiv(groups, cpr));
+  // four rows in flight per thread once that still gives every SM six CTAs
+  const bool many = R >= 148LL * 6 * 4 * rpb;
+  const dim3 grid((unsigned)(many ? 148 * 6 : cdiv(R, rpb)), (unsigned)cdiv(groups, cpr));
   ProfScope prof(PK_EMBEDDING, 0.0, (double)R * (sizeof(Id) + width * (double)(sizeof(Tt) + sizeof(To))), st);
-  auto go = [&](auto one, auto eight) {
-    launch_dependent(many ? eight : one, grid, dim3(kLookThreads), 0, st, (const Tt*)table, (uint32_t)n_rows, width,
+  auto go = [&](auto one, auto four) {
+    launch_dependent(many ? four : one, grid, dim3(kLookThreads), 0, st, (const Tt*)table, (uint32_t)n_rows, width,
                      (const Id*)ids, R, cpr, scale, (To*)out, out_ld);
   };
   switch (ve) {
-    case 8: go(emb_lookup_kernel<Tt, To, Id, 8, 1>, emb_lookup_kernel<Tt, To, Id, 8, 8>); break;
-    case 4: go(emb_lookup_kernel<Tt, To, Id, 4, 1>, emb_lookup_kernel<Tt, To, Id, 4, 8>); break;
-    case 2: go(emb_lookup_kernel<Tt, To, Id, 2, 1>, emb_lookup_kernel<Tt, To, Id, 2, 8>); break;
-    default: go(emb_lookup_kernel<Tt, To, Id, 1, 1>, emb_lookup_kernel<Tt, To, Id, 1, 8>); break;
+    case 8: go(emb_lookup_kernel<Tt, To, Id, 8, 1>, emb_lookup_kernel<Tt, To, Id, 8, 4>); break;
+    case 4: go(emb_lookup_kernel<Tt, To, Id, 4, 1>, emb_lookup_kernel<Tt, To, Id, 4, 4>); break;
+    case 2: go(emb_lookup_kernel<Tt, To, Id, 2, 1>, emb_lookup_kernel<Tt, To, Id, 2, 4>); break;
+    default: go(emb_lookup_kernel<Tt, To, Id, 1, 1>, emb_lookup_kernel<Tt, To, Id, 1, 4>); break;
   }
   return last_launch();
 }
@@ -443,7 +443,6 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   a.events = c->events; a.weights = c->weights; a.dtokens = c->dtokens; a.rows = c->rows; a.devents = c->devents;
   ProfScope prof(PK_ROUTED_GRAD, 2.0 * R * k * (3.0 * e * d + 2.0 * d * d), (double)R * (2 * e + d) * m->es, st);
   const unsigned gy = (unsigned)(cap / 64);
-  launch_dependent(routed_simt_kernel<T, Td, RS_HIDDEN_GRAD>, dim3(nb, gy), dim3(256), 0, st, a);
   launch_dependent(routed_simt_kernel<T, Td, RS_DU>, dim3(nb, gy), dim3(256), 0, st, a);
   launch_dependent(routed_wgrad_simt_kernel<T, Td>, dim3(n2 + n1, w1.slices), dim3(256), 0, st, a, w1, w2, n2);
   OT_TRY(last_launch());

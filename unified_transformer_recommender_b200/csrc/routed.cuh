@@ -199,8 +199,7 @@ template <typename T, typename Td> __device__ inline float operand(Td v) { retur
 enum RoutedStep : int {
   RS_HIDDEN,      // u = e W1^T + b1: z -> buf0
   RS_TOKEN,       // y = z W2^T + b2 + emb, times w -> token rows (k = 1) or part[choice]
-  RS_HIDDEN_GRAD, // u = e W1^T + b1: z -> buf0, GELU'(u) -> buf1
-  RS_DU,          // dz = dtoken W2: w dz g -> buf1, w z -> buf0, <dz, z> over 64 columns -> dot
+  RS_DU,          // u = e W1^T + b1 and dz = dtoken W2: w z -> buf0, w dz GELU'(u) -> buf1, <dz, z> over 64 columns -> dot
   RS_DEVENT       // de = du W1 -> event rows (k = 1) or part[choice]
 };
 
@@ -219,11 +218,87 @@ struct RoutedArgs {
   float* dot;                  // [slots][d / 64 rounded up]
 };
 
-// 64 slots x 64 columns per CTA, 16 of the contraction at a time, 4 x 4
-// results per thread.  T: the mode's type, Td: the type of dtokens.
+// 64 slots x 64 columns per CTA, 32 of the contraction at a time, 4 x 4
+// results per thread; the next 32 are loaded into registers during this one's
+// sums.  RS_DU runs two products one after the other.  T: the mode's type, Td:
+// the type of dtokens.
+constexpr int kSimtK = 32;
+
+// Four neighbouring elements p[0 .. 3], those past n zero; vec: 4-element
+// accesses are aligned (and n a multiple of 4).
+template <typename T>
+__device__ inline void load_four(const T* p, int n, bool vec, float* v) {
+  if (vec) {
+    if (n > 0) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 q = *(const float4*)p;
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+      } else {
+        const uint2 q = *(const uint2*)p;
+        v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+        v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+      }
+    } else {
+      v[0] = v[1] = v[2] = v[3] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
+  }
+}
+
+// acc += A B over the contraction K: A rows arow (null: zero), B K-major
+// (b + n * K) or not (b + k * N).
+template <typename Ta, typename Tb, bool B_KMAJOR, typename Round>
+__device__ inline void simt_product(float (*As)[68], float (*Bs)[68], float (*acc)[4], const Ta* arow, const Tb* b, int K,
+                                    int N, int n0, bool vec, Round round) {
+  const int ar = threadIdx.x >> 2, ak = (threadIdx.x & 3) * 4;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  float av[2][4], bv[2][4];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int kk = k0 + h * 16 + ak;
+      load_four(arow + kk, arow ? K - kk : 0, vec, av[h]);
+      if constexpr (B_KMAJOR) {           // n = ar, contraction = kk
+        load_four(b + (long long)(n0 + ar) * K + kk, n0 + ar < N ? K - kk : 0, vec, bv[h]);
+      } else {                            // contraction = ty, n = tx * 4
+        const int kb = k0 + h * 16 + ty, n = n0 + tx * 4;
+        load_four(b + (long long)kb * N + n, kb < K ? N - n : 0, vec, bv[h]);
+      }
+    }
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < K; k0 += kSimtK) {
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) As[h * 16 + ak + i][ar] = round(av[h][i]);
+      if constexpr (B_KMAJOR) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Bs[h * 16 + ak + i][ar] = bv[h][i];
+      } else {
+        *(float4*)&Bs[h * 16 + ty][tx * 4] = make_float4(bv[h][0], bv[h][1], bv[h][2], bv[h][3]);
+      }
+    }
+    __syncthreads();
+    fetch(k0 + kSimtK);                   // past K: zeros, no access
+#pragma unroll 8
+    for (int kk = 0; kk < kSimtK; ++kk) {
+      const float4 x = *(const float4*)&As[kk][ty * 4], w = *(const float4*)&Bs[kk][tx * 4];
+      const float xs[4] = {x.x, x.y, x.z, x.w}, wsv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], wsv[j], acc[i][j]);
+    }
+  }
+}
+
 template <typename T, typename Td, int STEP>
 __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
-  __shared__ __align__(16) float As[16][68], Bs[16][68];
+  __shared__ __align__(16) float As[kSimtK][68], Bs[kSimtK][68];
   __shared__ int s_flat[64];
   grid_dep_wait();
   grid_dep_launch();
@@ -232,68 +307,31 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
   if (s0 >= plan_first(a.plan, a.plan.T)) return;
   const int t = plan_type(a.plan, s0);
   // a tile of padding only has nothing to store but the zeros of the backward's buffers
-  constexpr bool ZEROS = STEP == RS_HIDDEN_GRAD || STEP == RS_DU;
-  if (!ZEROS && s0 >= plan_first(a.plan, t) + plan_count(a.plan, t)) return;
-  const int n0 = blockIdx.x * 64;
-  const int K = STEP == RS_HIDDEN || STEP == RS_HIDDEN_GRAD ? a.e : a.d;
-  const int N = STEP == RS_DEVENT ? a.e : a.d;
+  if (STEP != RS_DU && s0 >= plan_first(a.plan, t) + plan_count(a.plan, t)) return;
+  const int n0 = blockIdx.x * 64, N = STEP == RS_DEVENT ? a.e : a.d;
   if (threadIdx.x < 64) s_flat[threadIdx.x] = a.plan.order[s0 + threadIdx.x];
   __syncthreads();
   const int k = a.plan.k;
-  const int ar = threadIdx.x >> 2, ak = (threadIdx.x & 3) * 4;   // A: row, 4 of the contraction
-  const int aflat = s_flat[ar];
+  const int ar = threadIdx.x >> 2, aflat = s_flat[ar];
   const T* W1 = (const T*)a.mlp.W1[t];
   const T* W2 = (const T*)a.mlp.W2[t];
-  constexpr bool B_KMAJOR = STEP == RS_HIDDEN || STEP == RS_HIDDEN_GRAD || STEP == RS_TOKEN;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const long long aoff = STEP == RS_DU && aflat >= 0 ? token_off(a.rows, aflat / k, a.d) : 0;
-  float acc[4][4] = {}, av[4], bv[4];
-  auto fetch = [&](int k0) {     // this thread's operands of step k0, into registers
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int kk = k0 + ak + i;
-      float v = 0.f;
-      if (aflat >= 0 && kk < K) {
-        if constexpr (STEP == RS_HIDDEN || STEP == RS_HIDDEN_GRAD)
-          v = to_f(((const T*)a.events)[(long long)(aflat / k) * a.e + kk]);
-        else if constexpr (STEP == RS_TOKEN) v = a.buf0[(long long)(s0 + ar) * a.d + kk];
-        else if constexpr (STEP == RS_DU) v = operand<T>(((const Td*)a.dtokens)[aoff + kk]);
-        else v = a.buf1[(long long)(s0 + ar) * a.d + kk];
-      }
-      av[i] = v;
-      float w = 0.f;
-      if constexpr (B_KMAJOR) {           // n = ar, contraction = ak + i
-        const int n = n0 + ar;
-        if (n < N && kk < K) w = to_f((STEP == RS_TOKEN ? W2 : W1)[(long long)n * K + kk]);
-      } else {                            // contraction = ty, n = tx * 4 + i
-        const int kb = k0 + ty, n = n0 + tx * 4 + i;
-        if (n < N && kb < K) w = to_f((STEP == RS_DU ? W2 : W1)[(long long)kb * N + n]);
-      }
-      bv[i] = w;
-    }
-  };
-  fetch(0);
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) As[ak + i][ar] = av[i];
-    if constexpr (B_KMAJOR) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) Bs[ak + i][ar] = bv[i];
-    } else {
-      *(float4*)&Bs[ty][tx * 4] = make_float4(bv[0], bv[1], bv[2], bv[3]);
-    }
-    __syncthreads();
-    fetch(k0 + 16);               // in flight over this step's sums (past K: zeros, no access)
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk) {
-      const float4 x = *(const float4*)&As[kk][ty * 4], w = *(const float4*)&Bs[kk][tx * 4];
-      const float xs[4] = {x.x, x.y, x.z, x.w}, wsv[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], wsv[j], acc[i][j]);
-    }
+  const bool vec = a.e % 4 == 0 && a.d % 4 == 0 && a.rows.sample_ld % 4 == 0;
+  auto same = [](float x) { return x; };
+  float acc[4][4] = {}, u[STEP == RS_DU ? 4 : 1][4] = {};
+  const T* erow = aflat >= 0 ? (const T*)a.events + (long long)(aflat / k) * a.e : nullptr;
+  const float* r0 = a.buf0 + (long long)(s0 + ar) * a.d;
+  const float* r1 = a.buf1 + (long long)(s0 + ar) * a.d;
+  if constexpr (STEP == RS_HIDDEN) {
+    simt_product<T, T, true>(As, Bs, acc, erow, W1, a.e, N, n0, vec, same);
+  } else if constexpr (STEP == RS_TOKEN) {
+    simt_product<float, T, true>(As, Bs, acc, aflat >= 0 ? r0 : nullptr, W2, a.d, N, n0, vec, same);
+  } else if constexpr (STEP == RS_DEVENT) {
+    simt_product<float, T, false>(As, Bs, acc, aflat >= 0 ? r1 : nullptr, W1, a.d, N, n0, vec, same);
+  } else {
+    const Td* yrow = aflat >= 0 ? (const Td*)a.dtokens + token_off(a.rows, aflat / k, a.d) : nullptr;
+    simt_product<T, T, true>(As, Bs, u, erow, W1, a.e, N, n0, vec, same);
+    simt_product<Td, T, false>(As, Bs, acc, yrow, W2, a.d, N, n0, vec, [](float x) { return to_f(from_f<T>(x)); });
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -306,16 +344,16 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
       const int n = n0 + tx * 4 + j;
       if (n >= N) continue;
       const float v = acc[i][j];
-      if constexpr (STEP == RS_HIDDEN || STEP == RS_HIDDEN_GRAD) {
-        float z = 0.f, g = 0.f;
-        if (flat >= 0) gelu_and_slope(v + to_f(((const T*)a.mlp.b1[t])[n]), z, g);
-        a.buf0[slot * a.d + n] = z;
-        if constexpr (STEP == RS_HIDDEN_GRAD) a.buf1[slot * a.d + n] = g;
+      if constexpr (STEP == RS_HIDDEN) {
+        float z, g;
+        gelu_and_slope(v + to_f(((const T*)a.mlp.b1[t])[n]), z, g);
+        a.buf0[slot * a.d + n] = flat < 0 ? 0.f : z;
       } else if constexpr (STEP == RS_DU) {
-        const float z = a.buf0[slot * a.d + n];
+        float z = 0.f, g = 0.f;
+        if (flat >= 0) gelu_and_slope(u[i][j] + to_f(((const T*)a.mlp.b1[t])[n]), z, g);
         dot = fmaf(v, z, dot);
         a.buf0[slot * a.d + n] = flat < 0 ? 0.f : w * z;
-        a.buf1[slot * a.d + n] = flat < 0 ? 0.f : w * v * a.buf1[slot * a.d + n];
+        a.buf1[slot * a.d + n] = flat < 0 ? 0.f : w * v * g;
       } else if (flat >= 0) {
         if constexpr (STEP == RS_TOKEN) {
           const float y = v + (to_f(((const T*)a.mlp.b2[t])[n]) + to_f(((const T*)a.mlp.emb)[(long long)t * a.d + n]));
