@@ -53,6 +53,8 @@ def make_ids(kind, R, V, seed, dtype=torch.int32):
     ("fp32", "bf16", torch.int64, 129, 70, 7, 2),
     ("fp32", "fp32", torch.int32, 2049, 100, 300, 0),
     ("bf16", "bf16", torch.int32, 70001, 5003, 16, 0),
+    ("fp32", "fp32", torch.int64, 37, 20, 5000, 0),      # rows wider than a CTA
+    ("bf16", "fp32", torch.int32, 100_001, 77, 12, 4),   # many rows, each CTA walking
 ])
 def test_lookup(mode, table_t, ids_t, R, V, w, pad):
     g = torch.Generator(device="cuda").manual_seed(R)
@@ -163,6 +165,23 @@ def test_gradient_sparse(kind, dout_t, ids_t, R, V, w):
     again = torch.zeros_like(rows)
     ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, again, n, ws, scale=0.3)
     assert torch.equal(again[:U], rows[:U])                       # a fixed order of additions
+
+
+@pytest.mark.parametrize("R,V,w", [(200, 37, 9), (9000, 4000, 48), (30_000, 50, 20), (70_000, 300, 200)])
+def test_gradient_writes_nothing_past_its_outputs(R, V, w):
+    """Widths that leave lanes without a column, scale 1: elements behind the last row stay as they were."""
+    m = model("fp32")
+    dout = torch.randn(R, w, device="cuda")
+    ids = make_ids("popular", R, V, R + 5)
+    ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w)
+    buf = torch.full((V * w + 4096,), 7.0, device="cuda")
+    ot.onetrans_embedding_backward(m, dout, ids, buf[:V * w].view(V, w), ws)
+    assert (buf[V * w:] == 7.0).all()
+    check_rows(buf[:V * w].view(V, w), *reference(dout, ids, V, 1.0))
+    rows = torch.full((V * w + 4096,), 7.0, device="cuda")
+    uniq, n = torch.zeros(V, device="cuda", dtype=torch.int32), torch.zeros(1, device="cuda", dtype=torch.int32)
+    ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, rows[:V * w].view(V, w), n, ws)
+    assert (rows[int(n.item()) * w:] == 7.0).all()
 
 
 @pytest.mark.parametrize("kind,dout_t,ids_t,R,V,w", [c for c in GRADS if c[4] <= 2_000_000])

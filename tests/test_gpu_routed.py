@@ -162,6 +162,10 @@ CASES = [
     ("bf16", 513, 2, 1, 20, 96, True, "skewed"),       # widths the tensor-core kernels do not take
     ("bf16", 777, 3, 8, 48, 320, True, "skewed"),
     ("bf16", 260, 2, 1, 64, 512, False, "skewed"),
+    ("bf16", 700, 3, 2, 128, 384, True, "skewed"),     # the smallest rings
+    ("bf16", 900, 2, 1, 96, 320, True, "uniform"),
+    ("bf16", 1500, 3, 1, 64, 192, False, "skewed"),
+    ("bf16", 640, 2, 2, 128, 64, True, "skewed"),
     ("bf16", 30_000, 3, 1, 64, 256, True, "skewed"),
     ("bf16", 20_011, 8, 2, 64, 384, True, "skewed"),
 ]
@@ -227,7 +231,7 @@ def test_gradients(mode, R, T, k, e, d, weighted, kind):
 
 def test_plan_is_a_stable_sort():
     m, _ = make("fp32", 5, 8, 16, 3)
-    for R, k in ((1, 1), (127, 3), (1024, 1), (1025, 1), (20_000, 2)):
+    for R, k in ((1, 1), (127, 3), (1024, 1), (1025, 1), (20_000, 2), (700_001, 2)):   # the last past a million choices
         types = make_types("skewed", R, k, 5, R)
         plan = m.input_workspace(ot.OP_ROUTE, R, k)
         ot.onetrans_route_events(m, types, plan)
@@ -246,6 +250,34 @@ def test_plan_is_a_stable_sort():
             at = end
         assert p[16 + 5] == at and (pos[t < 0] == -1).all()
     assert ot.onetrans_device_status() == 0
+
+
+@pytest.mark.parametrize("d,e,k", [(256, 64, 1), (384, 32, 3)])
+def test_both_kernel_sets(d, e, k):
+    """The same call on tensor cores and (kernel policy 1) on CUDA cores, each within the bounds."""
+    m, W, ev, types, wt, plan, g = inputs("bf16", 1300, 4, k, e, d, True, "skewed")
+    dy = torch.randn(1300, d, device="cuda", generator=g).bfloat16()
+    ot.onetrans_route_events(m, types, plan)
+    ws, wsb = m.input_workspace(ot.OP_ROUTED, 1300, k), m.input_workspace(ot.OP_ROUTED_BACKWARD, 1300, k)
+    ftok, ttok = forward_ref(W, ev, types, wt, "bf16")
+    ref, tol = backward_ref(W, ev, types, wt, dy, dy, "bf16")
+    try:
+        for policy in (0, 1):
+            ot.onetrans_set_kernel_policy(policy)
+            tok = torch.empty(1300, d, device="cuda", dtype=torch.bfloat16)
+            ot.onetrans_tokenize_routed(m, ev, types, wt, plan, tok, ws)
+            close(tok, ftok, ttok, "tokens")
+            grads = {f: [torch.empty(tuple(x.shape), device="cuda") for x in W[f]] for f in ("Wb1", "bb1", "Wb2", "bb2")}
+            grads["type_emb"] = torch.empty(4, d, device="cuda")
+            de, dw = torch.empty_like(ev), torch.empty(1300, k, device="cuda")
+            ot.onetrans_tokenize_routed_backward(m, ev, types, wt, plan, dy, de, dw, grads, wsb)
+            close(de, ref["devents"], tol["devents"], "devents")
+            close(dw, ref["dweights"], tol["dweights"], "dweights")
+            for f in ("Wb1", "bb1", "Wb2", "bb2"):
+                close(torch.stack(grads[f]), ref[f], tol[f], f)
+            assert ot.onetrans_device_status() == 0
+    finally:
+        ot.onetrans_set_kernel_policy(0)
 
 
 def test_types_out_of_range_are_flagged_and_take_no_part():

@@ -223,7 +223,7 @@ static PlanBuf plan_buf(const onetrans_model* m, void* base, long long R, int k)
   p.head = (int*)cv.take(kPlanHeader * sizeof(int));
   p.order = (int*)cv.take((size_t)p.cap * sizeof(int));
   p.pos = (int*)cv.take((size_t)n * sizeof(int));
-  p.counts = (int*)cv.take((size_t)p.tiles * kMaxTypes * sizeof(int));
+  p.counts = (int*)cv.take((size_t)(p.tiles + 1) * kMaxTypes * sizeof(int));   // and the totals
   p.bytes = cv.used;
   return p;
 }
@@ -269,8 +269,21 @@ static onetrans_status route_impl(const onetrans_model* m, const int32_t* types,
   ProfScope prof(PK_ROUTE, 0.0, (double)n * 12, st);
   if (p.tiles > 1)
     launch_dependent(route_count_kernel, dim3(p.tiles), dim3(kRouteThreads), 0, st, types, n, T, p.counts);
+  // every CTA adding up all tiles' counts costs tiles^2 reads; past a million
+  // choices a scan does it once
+  int* tot = nullptr;
+  if (p.tiles > 1024) {
+    SortArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.tiles = p.tiles;
+    a.bits = 3;
+    a.hist = p.counts;
+    a.tot = tot = p.counts + (size_t)p.tiles * kMaxTypes;
+    static_assert(kMaxTypes == 8, "three bits of behaviour");
+    launch_dependent(sort_scan_kernel, dim3(1), dim3(1024), 0, st, a);
+  }
   launch_dependent(route_place_kernel, dim3(p.tiles), dim3(kRouteThreads), 0, st, types, n, (int)R, k, T,
-                   (const int*)p.counts, p.head, p.order, p.pos);
+                   (const int*)p.counts, (const int*)tot, p.head, p.order, p.pos);
   return last_launch();
 }
 

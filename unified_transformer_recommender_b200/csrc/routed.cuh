@@ -97,9 +97,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const int* _
 }
 
 // Places the tile's choices behind those of the same behaviour in the tiles
-// before.  With one tile it counts by itself (counts is not read).
+// before.  With one tile it counts by itself (counts is not read); with many
+// (tot not null) counts holds the prefixes over the tiles already and tot the
+// behaviours' totals, else each CTA adds up all tiles' counts.
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int* __restrict__ types, int n, int R, int k,
                                                                     int T, const int* __restrict__ counts,
+                                                                    const int* __restrict__ tot,
                                                                     int* __restrict__ plan, int* __restrict__ order,
                                                                     int* __restrict__ pos) {
   constexpr int NW = kRouteThreads / 32;
@@ -117,7 +120,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int* _
   const int i0 = blockIdx.x * kRouteTile + warp * kRouteItems * 32 + lane;
 #pragma unroll
   for (int u = 0; u < kRouteItems; ++u) ty[u] = route_type(types, i0 + u * 32, n, T);
-  if (gridDim.x > 1) {
+  if (tot) {
+    if (threadIdx.x < kMaxTypes) {
+      s_all[threadIdx.x] = tot[threadIdx.x];
+      s_before[threadIdx.x] = counts[blockIdx.x * kMaxTypes + threadIdx.x];
+    }
+  } else if (gridDim.x > 1) {
     int all = 0, before = 0;   // thread i always meets behaviour i % 8
 #pragma unroll 4
     for (int i = threadIdx.x; i < (int)gridDim.x * kMaxTypes; i += kRouteThreads) {

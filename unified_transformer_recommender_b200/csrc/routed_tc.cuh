@@ -483,12 +483,12 @@ __device__ inline float rcp_ftz(float x) {
 }
 // GELU-tanh and its slope of a pair, to float32 accuracy: with
 // s = 1 / (1 + exp(-2v)), v = c (u + a u^3), GELU(u) = u s and
-// d/du = s + u s (1 - s) (2c + 6 c a u^2)  (0.5 (1 + tanh v) = s).  The
-// special-function unit (16 results a clock an SM) bounds these loops, so the
-// two reciprocals of a pair come from one, 1/p = q / (p q); the exponent is
-// held at 2^63 for that (s >= 2^-63 in place of 0: GELU off by |u| 2^-63).
-// The rest runs on packed float32 pairs.  u^2 is bounded in the slope, where
-// inf * 0 would follow for large |u|.
+// d/du = s + u s (1 - s) (2c + 6 c a u^2)  (0.5 (1 + tanh v) = s).  Two
+// special-function results a value (16 a clock an SM), the rest on packed
+// float32 pairs; one reciprocal for the two values of a pair (1/p = q / (p q))
+// saved special-function time but cost more in moves and bounds.  |u| large
+// gives s = 0 or 1 exactly; u^2 is bounded in the slope, where inf * 0 would
+// follow.
 struct GeluPair {
   uint64_t u2, s, z;
 };
@@ -499,10 +499,9 @@ __device__ __forceinline__ GeluPair gelu_pair(uint64_t u) {
   const uint64_t v = f2_mul(u, f2_fma(r.u2, f2_pack(m2l * c * a, m2l * c * a), f2_pack(m2l * c, m2l * c)));
   float x, y;
   f2_unpack(v, x, y);
-  const uint64_t d = f2_add(f2_pack(ex2_ftz(fminf(x, 63.f)), ex2_ftz(fminf(y, 63.f))), f2_pack(1.f, 1.f));
+  const uint64_t d = f2_add(f2_pack(ex2_ftz(x), ex2_ftz(y)), f2_pack(1.f, 1.f));
   f2_unpack(d, x, y);
-  const float q = rcp_ftz(x * y);
-  r.s = f2_mul(f2_pack(y, x), f2_pack(q, q));
+  r.s = f2_pack(rcp_ftz(x), rcp_ftz(y));
   r.z = f2_mul(u, r.s);
   return r;
 }
