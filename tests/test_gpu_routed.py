@@ -231,7 +231,7 @@ def test_gradients(mode, R, T, k, e, d, weighted, kind):
 
 def test_plan_is_a_stable_sort():
     m, _ = make("fp32", 5, 8, 16, 3)
-    for R, k in ((1, 1), (127, 3), (1024, 1), (1025, 1), (20_000, 2), (700_001, 2)):   # the last past a million choices
+    for R, k in ((1, 1), (127, 3), (1024, 1), (1025, 1), (20_000, 2), (700_001, 2), (1_400_001, 2)):   # the last with scanned counts
         types = make_types("skewed", R, k, 5, R)
         plan = m.input_workspace(ot.OP_ROUTE, R, k)
         ot.onetrans_route_events(m, types, plan)

@@ -617,8 +617,9 @@ def onetrans_tokenize_routed_backward(model: Model, events: torch.Tensor, types:
     keep = []
     for f, n in (("Wb1", d * e), ("bb1", d), ("Wb2", d * d), ("bb2", d)):
         ts = grads[f]
-        _need(len(ts) == T and all(t.numel() == n and t.is_contiguous() and t.dtype == torch.float32 and t.is_cuda for t in ts),
+        _need(len(ts) == T and all(t.numel() == n and t.is_contiguous() and t.dtype == torch.float32 for t in ts),
               f"grads['{f}'] must hold one contiguous float32 tensor of the weight's shape per behavior")
+        _on_one_device(*ts)
         arr = (P * T)(*[t.data_ptr() for t in ts])
         keep.append(arr)
         setattr(g, f, ctypes.cast(arr, PP))

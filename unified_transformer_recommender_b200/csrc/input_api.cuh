@@ -24,9 +24,11 @@ static onetrans_status lookup_impl(const void* table, long long n_rows, int widt
   int ve = sizeof(Tt) == 4 && sizeof(To) == 4 ? 4 : 8;
   while (width % ve || out_ld % ve) ve >>= 1;
   const int groups = width / ve, cpr = std::min(groups, kLookThreads), rpb = kLookThreads / cpr;
-  // four rows in flight per thread once that still gives every SM six CTAs
-  const bool many = R >= 148LL * 6 * 4 * rpb;
-  const dim3 grid((unsigned)(many ? 148 * 6 : cdiv(R, rpb)), (unsigned)cdiv(groups, cpr));
+  // four rows in flight per thread once that still gives every SM two CTAs
+  // (rows of 64 bf16, one row against four: 8192 2.1 / 2.3 us, 65536 4.3 / 4.0,
+  // 131072 6.8 / 5.1, 2^20 63 / 49)
+  const bool many = R >= 148LL * 2 * 4 * rpb;
+  const dim3 grid((unsigned)(many ? std::min(148LL * 6, cdiv(R, 4 * rpb)) : cdiv(R, rpb)), (unsigned)cdiv(groups, cpr));
   ProfScope prof(PK_EMBEDDING, 0.0, (double)R * (sizeof(Id) + width * (double)(sizeof(Tt) + sizeof(To))), st);
   auto go = [&](auto one, auto four) {
     launch_dependent(many ? four : one, grid, dim3(kLookThreads), 0, st, (const Tt*)table, (uint32_t)n_rows, width,
@@ -56,8 +58,12 @@ struct EmbGrad {
   int32_t* n_uniq;
 };
 
-// Sort items a thread: see the measurement at the sort kernels.
-static int sort_items(long long R) { return R <= 160 * 1024 ? 2 : R <= 320 * 1024 ? 4 : 8; }
+// Sort items a thread: the fewer a CTA ranks the sooner a pass is done, until
+// the tiles' counts cost more.  Whole sparse gradient of rows of 64, us:
+// 37000 ids 2 / 4 items 25.7 / 28.9, 75392 ids 31.6 / 32.0, 150000 ids 53.7 /
+// 42.9; 4 / 8 items: 327680 ids 89 / 98, 800000 ids 165 / 168, 2^20 ids 195 /
+// 191, 3 million 488 / 468.
+static int sort_items(long long R) { return R <= 80 * 1024 ? 2 : R < 1 << 20 ? 4 : 8; }
 
 static int key_bits(long long n_rows) {
   int b = 1;
@@ -65,9 +71,11 @@ static int key_bits(long long n_rows) {
   return b;
 }
 
-// Tiles whose counts every CTA of a pass adds up itself; with more, a scan
-// kernel turns them into prefixes first (each CTA reads tiles x digits counts).
-static const int kSortDirectTiles = 192;
+// Tiles whose counts every CTA of a pass adds up itself (it reads tiles x
+// digits of them); with more, a scan kernel turns them into prefixes first, a
+// launch more a pass.  Direct / scanned, us: 74 tiles 31.6 / 37.0, 123 tiles
+// 72.6 / 66.9, 147 tiles 53.7 / 48.1.
+static const int kSortDirectTiles = 96;
 
 template <typename T, typename Id, bool DENSE>
 static onetrans_status emb_reduce_launch(const EmbGrad& g, ReduceArgs a, cudaStream_t st) {
@@ -95,9 +103,11 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
   const long long R = g.R;
   const int items = sort_items(R), tile = kSortThreads * items;
   const int tiles = (int)cdiv(R, tile);
-  // sorted positions a warp: few while that leaves all of them resident at once
-  // (4 CTAs an SM), at most 4096 chunks up to 2^20 positions
-  const int wrows = R <= 148 * 4 * 8 * kRedWarps ? 8 : R <= 1 << 19 ? 16 : 32 * (int)cdiv(R, 1 << 20);
+  // sorted positions a warp: 8 while that leaves all CTAs resident at once (4 an
+  // SM), then more as the joins of the chunks would cost (whole gradient, rows
+  // of 64: 1024 ids 8 / 32 positions 9.8 / 13.8 us, 75392 ids 8 / 16 33.8 / 31.4,
+  // 524288 ids 16 / 32 132 / 120); at most 4096 chunks
+  const int wrows = R <= 148 * 4 * 8 * kRedWarps ? 8 : R <= 320 * 1024 ? 16 : 32 * (int)cdiv(R, 1 << 20);
   const int chunk = kRedWarps * wrows;
   const int chunks = (int)cdiv(R, chunk);
   Carve cv(ws, ws_bytes);
@@ -269,10 +279,11 @@ static onetrans_status route_impl(const onetrans_model* m, const int32_t* types,
   ProfScope prof(PK_ROUTE, 0.0, (double)n * 12, st);
   if (p.tiles > 1)
     launch_dependent(route_count_kernel, dim3(p.tiles), dim3(kRouteThreads), 0, st, types, n, T, p.counts);
-  // every CTA adding up all tiles' counts costs tiles^2 reads; past a million
-  // choices a scan does it once
+  // every CTA adding up all tiles' counts costs tiles^2 reads; past 2.6 million
+  // choices a scan does it once (direct / scan: 1.5 million 16.3 / 19.8 us, 3
+  // million 33.2 / 31.8, 10 million 259 / 110)
   int* tot = nullptr;
-  if (p.tiles > 1024) {
+  if (p.tiles > 2560) {
     SortArgs a;
     std::memset(&a, 0, sizeof(a));
     a.tiles = p.tiles;
@@ -391,7 +402,7 @@ static onetrans_status tokenize_routed_impl(const onetrans_model* m, const Route
     }));
     return k > 1 ? combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st) : ONETRANS_OK;
   }
-  const dim3 grid((unsigned)cdiv(d, 64), (unsigned)(cap / 64));
+  const dim3 grid((unsigned)(cdiv(d, 64) * (cap / 64)));
   launch_dependent(routed_simt_kernel<T, T, RS_HIDDEN>, grid, dim3(256), 0, st, a);
   launch_dependent(routed_simt_kernel<T, T, RS_TOKEN>, grid, dim3(256), 0, st, a);
   OT_TRY(last_launch());
@@ -455,13 +466,12 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   a.e = e; a.d = d;
   a.events = c->events; a.weights = c->weights; a.dtokens = c->dtokens; a.rows = c->rows; a.devents = c->devents;
   ProfScope prof(PK_ROUTED_GRAD, 2.0 * R * k * (3.0 * e * d + 2.0 * d * d), (double)R * (2 * e + d) * m->es, st);
-  const unsigned gy = (unsigned)(cap / 64);
-  launch_dependent(routed_simt_kernel<T, Td, RS_DU>, dim3(nb, gy), dim3(256), 0, st, a);
+  launch_dependent(routed_simt_kernel<T, Td, RS_DU>, dim3((unsigned)(nb * (cap / 64))), dim3(256), 0, st, a);
   launch_dependent(routed_wgrad_simt_kernel<T, Td>, dim3(n2 + n1, w1.slices), dim3(256), 0, st, a, w1, w2, n2);
   OT_TRY(last_launch());
   OT_TRY(wsum_launch(a.plan, w1, w2, d, e, T_n, c->grads, st));
   if (c->devents) {
-    launch_dependent(routed_simt_kernel<T, Td, RS_DEVENT>, dim3(eb, gy), dim3(256), 0, st, a);
+    launch_dependent(routed_simt_kernel<T, Td, RS_DEVENT>, dim3((unsigned)(eb * (cap / 64))), dim3(256), 0, st, a);
     OT_TRY(last_launch());
     OT_TRY(combine_launch<T>(a.plan, a.part, e, c->devents, TokenRows{0x7fffffff, 0}, st));
   }

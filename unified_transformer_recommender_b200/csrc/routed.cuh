@@ -311,12 +311,13 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   if (!plan_ok(a.plan)) return;
-  const int s0 = blockIdx.y * 64;
+  // column blocks of a slot tile are neighbours (they share its rows)
+  const int N = STEP == RS_DEVENT ? a.e : a.d, blocks = (N + 63) / 64;
+  const int s0 = blockIdx.x / blocks * 64, block = blockIdx.x % blocks, n0 = block * 64;
   if (s0 >= plan_first(a.plan, a.plan.T)) return;
   const int t = plan_type(a.plan, s0);
   // a tile of padding only has nothing to store but the zeros of the backward's buffers
   if (STEP != RS_DU && s0 >= plan_first(a.plan, t) + plan_count(a.plan, t)) return;
-  const int n0 = blockIdx.x * 64, N = STEP == RS_DEVENT ? a.e : a.d;
   if (threadIdx.x < 64) s_flat[threadIdx.x] = a.plan.order[s0 + threadIdx.x];
   __syncthreads();
   const int k = a.plan.k;
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
     if constexpr (STEP == RS_DU) {
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);   // the row's 16 lanes
-      if (tx == 0) a.dot[slot * gridDim.x + blockIdx.x] = dot;
+      if (tx == 0) a.dot[slot * blocks + block] = dot;
     }
   }
 }
