@@ -134,9 +134,9 @@ typedef struct {
  *   grads: every weight gradient (zeros for a behaviour without events).
  * BF16 mode: float32 dtokens are rounded to bf16 as matrix operands; z and
  * the pre-activation gradient enter the weight gradients' products as two
- * bf16 terms (16 bits of significand), so those keep float32 quality, and the
- * event gradient's product as one.  R = 0
- * writes the zeros of grads.  The plan is checked as above. */
+ * bf16 terms (16 bits of significand), and the event gradient's product as
+ * one, rounded once more as devents are stored.  R = 0 writes the zeros of
+ * grads.  The plan is checked as above. */
 ONETRANS_API onetrans_status onetrans_tokenize_routed_backward(
     const onetrans_model* m, const void* events, const float* weights, int64_t R, int32_t k, const void* plan,
     size_t plan_bytes, const void* dtokens, int32_t dtokens_mode, int64_t rows_per_sample, int64_t sample_ld,

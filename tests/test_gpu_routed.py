@@ -496,3 +496,31 @@ def test_no_events():
     grads["type_emb"] = torch.full((2, 64), 9.0, device="cuda")
     ot.onetrans_tokenize_routed_backward(m, ev, types, None, plan, tok, None, None, grads, m.input_workspace(ot.OP_ROUTED_BACKWARD, 0, 1))
     assert all((x == 0).all() for f in ("Wb1", "bb1", "Wb2", "bb2") for x in grads[f]) and (grads["type_emb"] == 0).all()
+
+
+def test_more_slot_tiles_than_a_grid_dimension():
+    """4.2 million choices, 65552 tiles of 64 slots on CUDA cores: tokens and event gradient of every row."""
+    R, d, e = 64 * 65536 + 1000, 16, 1
+    m, W = make("fp32", 1, e, d, 71)
+    g = torch.Generator(device="cuda").manual_seed(72)
+    ev = torch.randn(R, e, device="cuda", generator=g)
+    types = torch.zeros(R, device="cuda", dtype=torch.int32)
+    wt = torch.ones(R, 1, device="cuda")
+    plan = m.input_workspace(ot.OP_ROUTE, R, 1)
+    ot.onetrans_route_events(m, types, plan)
+    tok = torch.empty(R, d, device="cuda")
+    ot.onetrans_tokenize_routed(m, ev, types, None, plan, tok, m.input_workspace(ot.OP_ROUTED, R, 1))
+    ref, tol = forward_ref(W, ev, types[:, None], wt, "fp32")
+    close(tok, ref, tol, "tokens")
+    del ref, tol
+    dy = torch.randn(R, d, device="cuda", generator=g)
+    de = torch.empty_like(ev)
+    grads = {f: [torch.empty(tuple(x.shape), device="cuda") for x in W[f]] for f in ("Wb1", "bb1", "Wb2", "bb2")}
+    grads["type_emb"] = torch.empty(1, d, device="cuda")
+    ot.onetrans_tokenize_routed_backward(m, ev, types, None, plan, dy, de, None, grads,
+                                         m.input_workspace(ot.OP_ROUTED_BACKWARD, R, 1))
+    ref, tol = backward_ref(W, ev, types[:, None], wt, dy, dy, "fp32")
+    close(de, ref["devents"], tol["devents"], "devents")
+    for f in ("Wb1", "bb1", "Wb2", "bb2"):
+        close(torch.stack(grads[f]), ref[f], tol[f], f)
+    assert ot.onetrans_device_status() == 0

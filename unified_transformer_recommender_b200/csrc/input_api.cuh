@@ -358,6 +358,18 @@ struct RoutedCall {
   RoutedGrads grads;
 };
 
+// One product of the CUDA-core path over `columns` output columns; see the
+// kernel for when two groups of threads share a CTA.
+template <typename T, typename Td, int STEP>
+static onetrans_status simt_launch(const RoutedArgs& a, int columns, long long cap, cudaStream_t st) {
+  const long long ctas = cdiv(columns, 64) * (cap / 64);
+  if (ctas <= 148 * 2)
+    launch_dependent(routed_simt_kernel<T, Td, STEP, 2>, dim3((unsigned)ctas), dim3(512), 0, st, a);
+  else
+    launch_dependent(routed_simt_kernel<T, Td, STEP, 1>, dim3((unsigned)ctas), dim3(256), 0, st, a);
+  return last_launch();
+}
+
 template <typename T>
 static onetrans_status tokenize_routed_impl(const onetrans_model* m, const RoutedCall* c, long long R, int k, void* ws,
                                             size_t ws_bytes, cudaStream_t st, size_t* need) {
@@ -402,10 +414,8 @@ static onetrans_status tokenize_routed_impl(const onetrans_model* m, const Route
     }));
     return k > 1 ? combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st) : ONETRANS_OK;
   }
-  const dim3 grid((unsigned)(cdiv(d, 64) * (cap / 64)));
-  launch_dependent(routed_simt_kernel<T, T, RS_HIDDEN>, grid, dim3(256), 0, st, a);
-  launch_dependent(routed_simt_kernel<T, T, RS_TOKEN>, grid, dim3(256), 0, st, a);
-  OT_TRY(last_launch());
+  OT_TRY((simt_launch<T, T, RS_HIDDEN>(a, d, cap, st)));
+  OT_TRY((simt_launch<T, T, RS_TOKEN>(a, d, cap, st)));
   return combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st);
 }
 
@@ -466,13 +476,12 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   a.e = e; a.d = d;
   a.events = c->events; a.weights = c->weights; a.dtokens = c->dtokens; a.rows = c->rows; a.devents = c->devents;
   ProfScope prof(PK_ROUTED_GRAD, 2.0 * R * k * (3.0 * e * d + 2.0 * d * d), (double)R * (2 * e + d) * m->es, st);
-  launch_dependent(routed_simt_kernel<T, Td, RS_DU>, dim3((unsigned)(nb * (cap / 64))), dim3(256), 0, st, a);
+  OT_TRY((simt_launch<T, Td, RS_DU>(a, d, cap, st)));
   launch_dependent(routed_wgrad_simt_kernel<T, Td>, dim3(n2 + n1, w1.slices), dim3(256), 0, st, a, w1, w2, n2);
   OT_TRY(last_launch());
   OT_TRY(wsum_launch(a.plan, w1, w2, d, e, T_n, c->grads, st));
   if (c->devents) {
-    launch_dependent(routed_simt_kernel<T, Td, RS_DEVENT>, dim3((unsigned)(eb * (cap / 64))), dim3(256), 0, st, a);
-    OT_TRY(last_launch());
+    OT_TRY((simt_launch<T, Td, RS_DEVENT>(a, e, cap, st)));
     OT_TRY(combine_launch<T>(a.plan, a.part, e, c->devents, TokenRows{0x7fffffff, 0}, st));
   }
   if (c->dweights)

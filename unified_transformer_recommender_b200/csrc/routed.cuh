@@ -77,7 +77,8 @@ __device__ inline int route_type(const int* types, int i, int n, int T) {
   return -1;
 }
 
-// counts[tile][8]: choices of each behaviour in the tile.
+// counts[tile][8]: choices of each behaviour in the tile.  Both plan kernels
+// are a launch and a few dependent loads: 75392 choices in 5.7 us together.
 __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const int* __restrict__ types, int n, int T,
                                                                     int* __restrict__ counts) {
   __shared__ int c[kMaxTypes];
@@ -226,11 +227,18 @@ struct RoutedArgs {
   float* dot;                  // [slots][d / 64 rounded up]
 };
 
-// 64 slots x 64 columns per CTA, 32 of the contraction at a time, 4 x 4
-// results per thread; the next 32 are loaded into registers during this one's
-// sums.  RS_DU runs two products one after the other.  T: the mode's type, Td:
-// the type of dtokens.
+// 64 slots x 64 columns per CTA, 4 x 4 results per thread of a group of 256;
+// the contraction goes in blocks of 32, the next block loaded into registers
+// during this one's sums.  RS_DU runs two products one after the other.  T: the
+// mode's type, Td: the type of dtokens.
+// Float32 sums on the CUDA cores bound it at many events.  With fewer than two
+// CTAs an SM a block of the contraction is a chain of latencies (load, store,
+// barrier, sums); two groups (GROUPS) then take the blocks in turn and add up
+// at the end, each for half of the rows.  Whole gradient (d 256, e 64), one /
+// two groups: 1178 events 85 / 69 us, 10000 events 218 / 232, 75392 events
+// 1217 / 1416.
 constexpr int kSimtK = 32;
+typedef float SimtTile[kSimtK][68];
 
 // Four neighbouring elements p[0 .. 3], those past n zero; vec: 4-element
 // accesses are aligned (and n a multiple of 4).
@@ -257,11 +265,14 @@ __device__ inline void load_four(const T* p, int n, bool vec, float* v) {
 
 // acc += A B over the contraction K: A rows arow (null: zero), B K-major
 // (b + n * K) or not (b + k * N).
-template <typename Ta, typename Tb, bool B_KMAJOR, typename Round>
-__device__ inline void simt_product(float (*As)[68], float (*Bs)[68], float (*acc)[4], const Ta* arow, const Tb* b, int K,
-                                    int N, int n0, bool vec, Round round) {
-  const int ar = threadIdx.x >> 2, ak = (threadIdx.x & 3) * 4;
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+template <int GROUPS, typename Ta, typename Tb, bool B_KMAJOR, typename Round>
+__device__ inline void simt_product(SimtTile* tiles, float (*acc)[4], const Ta* arow, const Tb* b, int K, int N, int n0,
+                                    bool vec, Round round) {
+  const int tid = threadIdx.x & 255, group = GROUPS == 2 ? threadIdx.x >> 8 : 0;
+  const int ar = tid >> 2, ak = (tid & 3) * 4;
+  const int ty = tid >> 4, tx = tid & 15;
+  SimtTile &As = tiles[group * 2], &Bs = tiles[group * 2 + 1];
+  auto group_sync = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(group + 1) : "memory"); };
   float av[2][4], bv[2][4];
   auto fetch = [&](int k0) {
 #pragma unroll
@@ -276,9 +287,9 @@ __device__ inline void simt_product(float (*As)[68], float (*Bs)[68], float (*ac
       }
     }
   };
-  fetch(0);
-  for (int k0 = 0; k0 < K; k0 += kSimtK) {
-    __syncthreads();
+  fetch(group * kSimtK);
+  for (int k0 = group * kSimtK; k0 < K; k0 += GROUPS * kSimtK) {
+    group_sync();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -290,8 +301,8 @@ __device__ inline void simt_product(float (*As)[68], float (*Bs)[68], float (*ac
         *(float4*)&Bs[h * 16 + ty][tx * 4] = make_float4(bv[h][0], bv[h][1], bv[h][2], bv[h][3]);
       }
     }
-    __syncthreads();
-    fetch(k0 + kSimtK);                   // past K: zeros, no access
+    group_sync();
+    fetch(k0 + GROUPS * kSimtK);          // past K: zeros, no access
 #pragma unroll 8
     for (int kk = 0; kk < kSimtK; ++kk) {
       const float4 x = *(const float4*)&As[kk][ty * 4], w = *(const float4*)&Bs[kk][tx * 4];
@@ -304,9 +315,27 @@ __device__ inline void simt_product(float (*As)[68], float (*Bs)[68], float (*ac
   }
 }
 
-template <typename T, typename Td, int STEP>
-__global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
-  __shared__ __align__(16) float As[kSimtK][68], Bs[kSimtK][68];
+// The two groups' sums of the thread's results, in acc[0] and acc[1]: rows 0
+// and 1 of them in group 0, rows 2 and 3 in group 1.  `to`: 2 x 8 x 256 floats
+// of shared memory.
+__device__ inline void simt_join(float* to, float (*acc)[4]) {
+  const int tid = threadIdx.x & 255, group = threadIdx.x >> 8;
+  float* mine = to + group * 2048 + tid;
+  const float* other = to + (group ^ 1) * 2048 + tid;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine[(i * 4 + j) * 256] = group ? acc[i][j] : acc[2 + i][j];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = (group ? acc[2 + i][j] : acc[i][j]) + other[(i * 4 + j) * 256];
+}
+
+template <typename T, typename Td, int STEP, int GROUPS>
+__global__ void __launch_bounds__(256 * GROUPS) routed_simt_kernel(RoutedArgs a) {
+  __shared__ __align__(16) SimtTile tiles[2 * GROUPS];
   __shared__ int s_flat[64];
   grid_dep_wait();
   grid_dep_launch();
@@ -321,10 +350,12 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
   if (threadIdx.x < 64) s_flat[threadIdx.x] = a.plan.order[s0 + threadIdx.x];
   __syncthreads();
   const int k = a.plan.k;
-  const int ar = threadIdx.x >> 2, aflat = s_flat[ar];
+  constexpr int ROWS = 4 / GROUPS;               // result rows a thread finishes
+  const int tid = threadIdx.x & 255, group = GROUPS == 2 ? threadIdx.x >> 8 : 0;
+  const int ar = tid >> 2, aflat = s_flat[ar];
   const T* W1 = (const T*)a.mlp.W1[t];
   const T* W2 = (const T*)a.mlp.W2[t];
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int ty = tid >> 4, tx = tid & 15;
   const bool vec = a.e % 4 == 0 && a.d % 4 == 0 && a.rows.sample_ld % 4 == 0;
   auto same = [](float x) { return x; };
   float acc[4][4] = {}, u[STEP == RS_DU ? 4 : 1][4] = {};
@@ -332,19 +363,25 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
   const float* r0 = a.buf0 + (long long)(s0 + ar) * a.d;
   const float* r1 = a.buf1 + (long long)(s0 + ar) * a.d;
   if constexpr (STEP == RS_HIDDEN) {
-    simt_product<T, T, true>(As, Bs, acc, erow, W1, a.e, N, n0, vec, same);
+    simt_product<GROUPS, T, T, true>(tiles, acc, erow, W1, a.e, N, n0, vec, same);
   } else if constexpr (STEP == RS_TOKEN) {
-    simt_product<float, T, true>(As, Bs, acc, aflat >= 0 ? r0 : nullptr, W2, a.d, N, n0, vec, same);
+    simt_product<GROUPS, float, T, true>(tiles, acc, aflat >= 0 ? r0 : nullptr, W2, a.d, N, n0, vec, same);
   } else if constexpr (STEP == RS_DEVENT) {
-    simt_product<float, T, false>(As, Bs, acc, aflat >= 0 ? r1 : nullptr, W1, a.d, N, n0, vec, same);
+    simt_product<GROUPS, float, T, false>(tiles, acc, aflat >= 0 ? r1 : nullptr, W1, a.d, N, n0, vec, same);
   } else {
     const Td* yrow = aflat >= 0 ? (const Td*)a.dtokens + token_off(a.rows, aflat / k, a.d) : nullptr;
-    simt_product<T, T, true>(As, Bs, u, erow, W1, a.e, N, n0, vec, same);
-    simt_product<Td, T, false>(As, Bs, acc, yrow, W2, a.d, N, n0, vec, [](float x) { return to_f(from_f<T>(x)); });
+    simt_product<GROUPS, T, T, true>(tiles, u, erow, W1, a.e, N, n0, vec, same);
+    simt_product<GROUPS, Td, T, false>(tiles, acc, yrow, W2, a.d, N, n0, vec, [](float x) { return to_f(from_f<T>(x)); });
+  }
+  if constexpr (GROUPS == 2) {
+    static_assert(sizeof(tiles) >= 2 * 4096 * sizeof(float), "room for both products' sums");
+    __syncthreads();
+    simt_join((float*)tiles, acc);
+    if constexpr (STEP == RS_DU) simt_join((float*)tiles + 4096, u);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = ty * 4 + i, flat = s_flat[row];
+  for (int i = 0; i < ROWS; ++i) {
+    const int row = ty * 4 + group * ROWS + i, flat = s_flat[row];
     const long long slot = s0 + row;
     const float w = flat < 0 ? 0.f : a.weights ? a.weights[flat] : 1.f;
     float dot = 0.f;
@@ -386,7 +423,8 @@ __global__ void __launch_bounds__(256) routed_simt_kernel(RoutedArgs a) {
 // out[r] = sum over the choices of part[r * k + j] (choices that are none
 // left out), rounded once.  k = 1: the products wrote the rows themselves,
 // and only rows without a behaviour are zeroed here.  A thread takes V
-// neighbouring columns of a row, the next row's choices behind this one's.
+// neighbouring columns of a row, four choices in flight.  Bound by reading
+// part: 20011 x 2 choices of 384 columns 14.5 us, 77 MB at 5.3 TB/s.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) routed_combine_kernel(PlanView plan, const float* __restrict__ part, int width,
                                                              T* __restrict__ out, TokenRows rows) {
@@ -440,7 +478,8 @@ __global__ void __launch_bounds__(256) routed_combine_kernel(PlanView plan, cons
 }
 
 // dweights[choice] = <dz, z> (in `parts` partial dots) + <dtoken, b2 + emb>;
-// 0 for a choice that is none.  One warp per choice.
+// 0 for a choice that is none.  One warp per choice, its loads in flight four
+// deep (a chain of latencies: place, behaviour, row).
 template <typename T, typename Td>
 __global__ void __launch_bounds__(256) routed_dweight_kernel(PlanView plan, RoutedMLP mlp, int d,
                                                              const Td* __restrict__ dtokens, TokenRows rows,
@@ -457,6 +496,7 @@ __global__ void __launch_bounds__(256) routed_dweight_kernel(PlanView plan, Rout
       const int t = plan_type(plan, slot);
       const Td* dy = dtokens + token_off(rows, (int)c / plan.k, d);
       const T *b2 = (const T*)mlp.b2[t], *emb = (const T*)mlp.emb + (long long)t * d;
+#pragma unroll 4
       for (int i = lane; i < d; i += 32) s = fmaf(to_f(dy[i]), to_f(b2[i]) + to_f(emb[i]), s);
       for (int i = lane; i < parts; i += 32) s += dot[(long long)slot * parts + i];
     }
@@ -480,7 +520,9 @@ __device__ inline float* piece_at(const WeightPieces& w, int s, int t) { return 
 
 // CUDA-core partial gradients: 64 x 64 of dW2 (blockIdx.x below n2) or dW1,
 // one slice, behaviour after behaviour.  The CTAs of the first column block
-// also add up db2 (dW2) or db1 (dW1) of their 64 rows.
+// also add up db2 (dW2) or db1 (dW1) of their 64 rows.  16 slots a step, the
+// next step's rows and the choices of the one after in flight: 1178 events (d
+// 256, e 64) 19 us, a chain of eight such steps.
 template <typename T, typename Td>
 __global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, WeightPieces w1, WeightPieces w2,
                                                                 int n2) {
@@ -503,8 +545,10 @@ __global__ void __launch_bounds__(256) routed_wgrad_simt_kernel(RoutedArgs a, We
     const int end = min(tile1 * 128, plan_first(a.plan, t + 1));
     if (lo >= end) continue;
     float acc[4][4] = {}, colsum = 0.f, av[4], bv[4], wt;
+    int ahead = lo + lr < hi ? a.plan.order[lo + lr] : -1;   // of the step fetched next
     auto fetch = [&](int s) {
-      const int slot = s + lr, flat = slot < hi ? a.plan.order[slot] : -1;
+      const int slot = s + lr, flat = ahead;
+      ahead = slot + 16 < hi ? a.plan.order[slot + 16] : -1;
       wt = flat < 0 ? 0.f : a.weights ? a.weights[flat] : 1.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) av[i] = bv[i] = 0.f;
@@ -561,7 +605,8 @@ struct RoutedGrads {
 
 // Each behaviour's pieces added in slice order (zeros where it has none);
 // blockIdx.y = behaviour, V neighbouring values a thread, eight pieces in
-// flight.  p1: dW1 and db1, p2: dW2 and db2.
+// flight.  p1: dW1 and db1, p2: dW2 and db2.  The pieces are mostly still in
+// L2: 39 pieces of d 256, e 64 in 3.9 us.
 template <int V>
 __global__ void __launch_bounds__(256) routed_wsum_kernel(PlanView plan, WeightPieces p1, WeightPieces p2, int d, int e,
                                                           RoutedGrads g) {
