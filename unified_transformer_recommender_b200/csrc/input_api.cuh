@@ -309,7 +309,10 @@ static onetrans_status combine_launch(const PlanView& plan, const float* part, i
   return last_launch();
 }
 
-// Shapes the tensor-core kernels take.
+// Shapes the tensor-core kernels take (d 256, e 64, tensor cores / CUDA cores:
+// tokens of 16 events 16.5 / 26.6 us, of 75392 29 / 453; gradient 39 / 47 and
+// 109 / 1272).  TMEM holds 512 columns: D of d and at least one U of 64 beside
+// it, or dW2 of d and one U of 128; the event rows are one or two boxes of 64.
 static bool routed_tc(const onetrans_model* m) {
   const int d = m->d, e = m->cfg.event_dim;
   return m->bf16 && d % 64 == 0 && d <= 384 && e % 16 == 0 && e <= 128;

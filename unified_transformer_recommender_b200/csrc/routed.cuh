@@ -18,7 +18,7 @@
 // This file: the plan, the CUDA-core kernels (float32 mode, and shapes the
 // tensor-core kernels do not take) and the passes both sets share.
 #pragma once
-#include "tc_ptx.cuh"
+#include "embedding.cuh"
 
 namespace ot {
 
@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(256) routed_combine_kernel(PlanView plan, cons
 }
 
 // dweights[choice] = <dz, z> (in `parts` partial dots) + <dtoken, b2 + emb>;
-// 0 for a choice that is none.  One warp per choice, its loads in flight four
-// deep (a chain of latencies: place, behaviour, row).
+// 0 for a choice that is none.  One warp per choice: a chain of latencies
+// (place, behaviour, row), so the row is read eight columns a lane.
 template <typename T, typename Td>
 __global__ void __launch_bounds__(256) routed_dweight_kernel(PlanView plan, RoutedMLP mlp, int d,
                                                              const Td* __restrict__ dtokens, TokenRows rows,
@@ -489,15 +489,32 @@ __global__ void __launch_bounds__(256) routed_dweight_kernel(PlanView plan, Rout
   grid_dep_launch();
   if (!plan_ok(plan)) return;
   const int lane = threadIdx.x & 31, n = plan.R * plan.k;
+  const bool vec = d % 8 == 0 && rows.sample_ld % 8 == 0;
+  int first[kMaxTypes - 1];      // where behaviours 1, 2, .. begin (all slots before those past the last)
+#pragma unroll
+  for (int i = 0; i < kMaxTypes - 1; ++i) first[i] = plan_first(plan, i + 1);
   for (long long c = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); c < n; c += (long long)gridDim.x * 8) {
     const int slot = plan.pos[c];
     float s = 0.f;
     if (slot >= 0) {
-      const int t = plan_type(plan, slot);
+      int t = 0;
+#pragma unroll
+      for (int i = 0; i < kMaxTypes - 1; ++i) t += slot >= first[i];
       const Td* dy = dtokens + token_off(rows, (int)c / plan.k, d);
       const T *b2 = (const T*)mlp.b2[t], *emb = (const T*)mlp.emb + (long long)t * d;
-#pragma unroll 4
-      for (int i = lane; i < d; i += 32) s = fmaf(to_f(dy[i]), to_f(b2[i]) + to_f(emb[i]), s);
+      if (vec) {
+#pragma unroll 2
+        for (int i = lane * 8; i < d; i += 256) {
+          float y[8], b[8], m[8];
+          emb_ld<8>(dy + i, y);
+          emb_ld<8>(b2 + i, b);
+          emb_ld<8>(emb + i, m);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) s = fmaf(y[n], b[n] + m[n], s);
+        }
+      } else {
+        for (int i = lane; i < d; i += 32) s = fmaf(to_f(dy[i]), to_f(b2[i]) + to_f(emb[i]), s);
+      }
       for (int i = lane; i < parts; i += 32) s += dot[(long long)slot * parts + i];
     }
 #pragma unroll
