@@ -55,6 +55,7 @@ def make_ids(kind, R, V, seed, dtype=torch.int32):
     ("bf16", "bf16", torch.int32, 70001, 5003, 16, 0),
     ("fp32", "fp32", torch.int64, 37, 20, 5000, 0),      # rows wider than a CTA
     ("bf16", "fp32", torch.int32, 100_001, 77, 12, 4),   # many rows, each CTA walking
+    ("bf16", "bf16", torch.int64, 300_001, 5003, 64, 0),
 ])
 def test_lookup(mode, table_t, ids_t, R, V, w, pad):
     g = torch.Generator(device="cuda").manual_seed(R)
@@ -136,6 +137,9 @@ GRADS = [
     ("uniform", "fp32", torch.int32, 270_001, 60_000, 20),  # more tiles than a pass adds up itself
     ("popular", "bf16", torch.int32, 300_000, 2_147_483_647, 8),   # three passes
     ("popular", "bf16", torch.int32, 1_100_000, 5_000, 16),        # chunks of more rows
+    ("uniform", "bf16", torch.int64, 100_003, 50_000, 12),         # four items a thread, counts added up by the passes
+    ("popular", "fp32", torch.int32, 400_000, 3_000, 8),           # the same with scanned counts
+    ("uniform", "bf16", torch.int32, 1 << 26, 1_000, 1),           # the most ids a call takes
 ]
 
 

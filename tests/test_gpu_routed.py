@@ -159,6 +159,8 @@ CASES = [
     ("bf16", 3001, 8, 3, 96, 384, True, "skewed"),
     ("bf16", 700, 4, 1, 128, 256, False, "last"),
     ("bf16", 300, 4, 2, 128, 384, True, "none"),
+    ("fp32", 10_007, 4, 2, 40, 80, True, "skewed"),    # many slot tiles on CUDA cores
+    ("bf16", 12_001, 3, 1, 20, 96, True, "uniform"),
     ("bf16", 513, 2, 1, 20, 96, True, "skewed"),       # widths the tensor-core kernels do not take
     ("bf16", 777, 3, 8, 48, 320, True, "skewed"),
     ("bf16", 260, 2, 1, 64, 512, False, "skewed"),
