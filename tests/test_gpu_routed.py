@@ -526,3 +526,38 @@ def test_more_slot_tiles_than_a_grid_dimension():
     for f in ("Wb1", "bb1", "Wb2", "bb2"):
         close(torch.stack(grads[f]), ref[f], tol[f], f)
     assert ot.onetrans_device_status() == 0
+
+
+@pytest.mark.parametrize("d,k", [(128, 1), (256, 1), (256, 2), (384, 2)])
+def test_choice_weights_reach_every_sum_exactly(d, k):
+    """Small whole choice weights through operands that make every product a whole number: W1 = 0 and b1 = 16 give
+    z = 16 and a slope of 1, W2 the identity gives dz = dtoken = 1.  Every gradient is then a sum of whole numbers
+    below 2^24 and has to be exact: one choice whose weight was read from another step would change it."""
+    T, e, R = 3, 64, 40_001
+    m, W = make("bf16", T, e, d, 91)
+    for t in range(T):
+        W["Wb1"][t].zero_()
+        W["bb1"][t].fill_(16.0)
+        W["Wb2"][t].copy_(torch.eye(d))
+        W["bb2"][t].zero_()
+    W["type_emb"].zero_()
+    g = torch.Generator(device="cuda").manual_seed(92)
+    ev = torch.ones(R, e, device="cuda", dtype=torch.bfloat16)
+    dy = torch.ones(R, d, device="cuda", dtype=torch.bfloat16)
+    plan, ws = m.input_workspace(ot.OP_ROUTE, R, k), m.input_workspace(ot.OP_ROUTED_BACKWARD, R, k)
+    for seed in range(6):
+        types = make_types("skewed", R, k, T, 93 + seed)
+        wt = torch.randint(1, 10, (R, k), device="cuda", generator=g).float()
+        ot.onetrans_route_events(m, types, plan)
+        grads = {f: [torch.full(tuple(x.shape), float("nan"), device="cuda") for x in W[f]] for f in ("Wb1", "bb1", "Wb2", "bb2")}
+        grads["type_emb"] = torch.full((T, d), float("nan"), device="cuda")
+        de, dw = torch.full_like(ev, float("nan")), torch.full((R, k), float("nan"), device="cuda")
+        ot.onetrans_tokenize_routed_backward(m, ev, types, wt, plan, dy, de, dw, grads, ws)
+        assert ot.onetrans_device_status() == 0
+        for t in range(T):
+            n = float(wt[types == t].sum())
+            assert 16 * n < 2 ** 24
+            for f, scale in (("Wb1", 1), ("bb1", 1), ("Wb2", 16), ("bb2", 1)):
+                assert (grads[f][t] == scale * n).all(), (seed, t, f)
+            assert (grads["type_emb"][t] == n).all()
+        assert (dw[types >= 0] == 16 * d).all() and (dw[types < 0] == 0).all() and (de == 0).all()

@@ -655,7 +655,8 @@ __device__ inline void wg_gather_events(const RoutedTcArgs& a, const WgCfg& cfg,
       }
       asm volatile("bar.sync 3, 64;" ::: "memory");
       if (ok) gather_events<64>(g, m.e + b * cfg.e_bytes, a.events, m.row + b * 128, a.e);
-      cp_async_arrive(&m.bars[WB_EFULL + b]);     // also releases the weights written above
+      cp_async_arrive(&m.bars[WB_EFULL + b]);
+      warp_arrive(&m.bars[WB_EFULL + b]);         // releases the weights: the arrival above covers the copies alone
       er.next(cfg.ebuf);
       wrapped = wrapped || er.s == 0;
     }
@@ -1149,7 +1150,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     auto init = [&](int bar, int n, int count) {
       for (int i = 0; i < n; ++i) mbar_init(&m.bars[bar + i], count);
     };
-    init(WB_EFULL, 3, 64);
+    init(WB_EFULL, 3, 64 + 2);     // every gather thread's copies, every gather warp's stores of the weights
     init(WB_EEMPTY, 3, role1 ? 1 : 1 + kWgCompute);
     init(WB_YFULL, 8, 128);
     init(WB_YEMPTY, 8, role1 ? 1 : 1 + kWgCompute);
