@@ -387,7 +387,8 @@ ONETRANS_API onetrans_status onetrans_device_status(void* stream, int32_t* code)
  * tensor-core kernel uses, limited to spin_limit try_wait rounds (1 ..
  * 2^20, else INVALID_ARG).  The wait gives up, records code 101 in the
  * device status word and the kernel returns; onetrans_device_status then
- * reports it. */
+ * reports it.  A warp whose lanes see different outcomes of a wait follows: it
+ * has to take it as run out in every lane (code 1 if one lane went on). */
 ONETRANS_API onetrans_status onetrans_selftest_bounded_wait(int32_t spin_limit, void* stream);
 /* Per-kernel timing for measurement.  While enabled, every launch is
  * bracketed by CUDA events on its stream and tagged with its kernel kind and

@@ -37,3 +37,14 @@ def test_bounded_wait_runs_out_and_reports():
     got = run_forward(b, X0)
     assert ot.onetrans_device_status() == 0
     assert rel_err(got, O.forward(X0, b.W, sh.L_NS, sh.n_heads, EPS, [sh.L_NS])) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("limit", [1, 7, 1000])
+def test_a_warp_leaves_a_wait_together(limit):
+    """Half of the self-test's lanes wait for a phase that is complete, half for one that never is: a product warp's
+    wait has run out for all of them (a lane that went on alone would wait in the next full-mask instruction; the
+    kernel records code 1 for it)."""
+    assert ot.onetrans_device_status() == 0
+    ot.onetrans_selftest_bounded_wait(limit)
+    assert ot.onetrans_device_status() == WAIT_TIMEOUT
+    assert ot.onetrans_device_status() == 0

@@ -1680,7 +1680,10 @@ static onetrans_status train_impl(const onetrans_model* m, const void* x0, int B
 // Failure path of the bounded waits, without a fault: one thread waits on an
 // mbarrier that nothing arrives at, with the same wait the tensor-core
 // kernels use but limited to `limit` rounds; the wait gives up, records
-// kErrWaitTimeout in the device status word, and the kernel returns.
+// kErrWaitTimeout in the device status word, and the kernel returns.  Then
+// the warp's wait with one outcome, where half of the lanes wait for a phase
+// that is complete and half for one that never is: no lane may go on as if the
+// wait had succeeded (that would be recorded as code 1).
 __global__ void selftest_wait_kernel(uint32_t limit) {
   __shared__ __align__(8) uint64_t bar;
   if (threadIdx.x == 0) {
@@ -1689,6 +1692,9 @@ __global__ void selftest_wait_kernel(uint32_t limit) {
   }
   __syncthreads();
   if (threadIdx.x == 0) mbar_wait_limited(&bar, 0, limit);
+  __syncwarp();
+  const bool through = mbar_wait_warp_limited(&bar, threadIdx.x < 16 ? 1 : 0, limit);
+  if (through) atomicExch(&g_device_status, 1);
 }
 
 // ============================================================== C ABI ====

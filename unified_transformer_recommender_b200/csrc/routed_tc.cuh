@@ -45,7 +45,8 @@ __device__ inline void fence_async_smem() { asm volatile("fence.proxy.async.shar
 // descriptors in uniform registers, where the tensor-core instructions want
 // them (a branch on the lane number costs a register move per operand).
 // elect.sync picks the same lane every time, so a commit covers the products
-// that lane issued.
+// that lane issued.  It names all 32 lanes: these warps wait with
+// mbar_wait_warp, so that no lane leaves a loop alone.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -313,9 +314,9 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     RingPos r, er;
     for (int tile = blockIdx.x; tile < n_tiles && ok; tile += step) {
       for (int c = 0; c < NC; ++c) {
-        ok = mbar_wait(&w_full[r.s], r.ph);      // refilled, so the slot's U is free too
+        ok = mbar_wait_warp(&w_full[r.s], r.ph);      // refilled, so the slot's U is free too
         if (c == 0) {
-          ok = ok && mbar_wait(&e_full[er.s], er.ph);
+          ok = ok && mbar_wait_warp(&e_full[er.s], er.ph);
           fence_async_smem();
         }
         if (!ok) break;
@@ -342,8 +343,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     int i = 0;
     for (int tile = blockIdx.x; tile < n_tiles && ok; tile += step, ++i) {
       for (int c = 0; c < NC; ++c) {
-        ok = mbar_wait(&z_ready[r.s], r.ph);
-        if (c == 0 && i > 0) ok = ok && mbar_wait(d_empty, (i - 1) & 1);
+        ok = mbar_wait_warp(&z_ready[r.s], r.ph);
+        if (c == 0 && i > 0) ok = ok && mbar_wait_warp(d_empty, (i - 1) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint64_t w2 = desc_add(dW, r.s * cfg.stage_bytes);
@@ -714,7 +715,7 @@ __device__ inline void wg_gather(const RoutedTcArgs& a, const WgCfg& cfg, const 
 template <int NC, bool ROLE1>
 __device__ inline bool wg_weights(const RoutedMaps& maps, const WgCfg& cfg, const WgShared& m, int t, int chunk, int p) {
   constexpr int d = NC * 64;
-  if (p > 0 && !mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1)) return false;
+  if (p > 0 && !mbar_wait_warp(&m.bars[WB_ACCFREE], (p - 1) & 1)) return false;
   if ((threadIdx.x & 31) == 0) {
     const uint64_t keep = l2_evict_last();
     uint64_t* full = &m.bars[WB_W];
@@ -727,7 +728,7 @@ __device__ inline bool wg_weights(const RoutedMaps& maps, const WgCfg& cfg, cons
         tma_load_3d_hint(&maps.w2[t], full, m.w2 + j * d * 128 + b * 8192, chunk * 128 + j * 64, b * 64, 0, keep);
   }
   __syncwarp();
-  return mbar_wait(&m.bars[WB_W], p & 1);
+  return mbar_wait_warp(&m.bars[WB_W], p & 1);
 }
 
 // Role 1's products.
@@ -752,8 +753,8 @@ __device__ inline void wg_products1(const RoutedMaps& maps, int chunk, const Rou
       ++p;
       for (int at = lo; at < hi; at += 128, ++i) {
         const int b = i & 1;
-        ok = ok && mbar_wait(&m.bars[WB_EFULL + er.s], er.ph);
-        if (i > 0) ok = ok && mbar_wait(&m.bars[WB_UFREE], (i - 1) & 1);   // U read into registers
+        ok = ok && mbar_wait_warp(&m.bars[WB_EFULL + er.s], er.ph);
+        if (i > 0) ok = ok && mbar_wait_warp(&m.bars[WB_UFREE], (i - 1) & 1);   // U read into registers
         if (!ok) break;
         fence_async_smem();
         tc_fence_after();
@@ -765,10 +766,10 @@ __device__ inline void wg_products1(const RoutedMaps& maps, int chunk, const Rou
             mma_ss(tU, desc_add(dW1, (k >> 2) * 16384 + (k & 3) * 32), desc_add(de, (k >> 2) * 16384 + (k & 3) * 32), id_u,
                    k ? 1u : 0u);
         mma_commit(&m.bars[WB_UFULL]);
-        if (i >= 2) ok = mbar_wait(&m.bars[WB_USED + b], ((i >> 1) & 1) ^ 1);
+        if (i >= 2) ok = mbar_wait_warp(&m.bars[WB_USED + b], ((i >> 1) & 1) ^ 1);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          ok = ok && mbar_wait(&m.bars[WB_YFULL + y.s], y.ph);
+          ok = ok && mbar_wait_warp(&m.bars[WB_YFULL + y.s], y.ph);
           if (!ok) break;
           fence_async_smem();
           tc_fence_after();
@@ -790,11 +791,11 @@ __device__ inline void wg_products1(const RoutedMaps& maps, int chunk, const Rou
   for (int t = 0; t < a.plan.T && ok; ++t) {
     int lo, hi;
     if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
-    if (p > 0) ok = mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1);
+    if (p > 0) ok = mbar_wait_warp(&m.bars[WB_ACCFREE], (p - 1) & 1);
     ++p;
     for (int at = lo; at < hi; at += 128, ++i) {
       const int b = i & 1;
-      ok = ok && mbar_wait(&m.bars[WB_READY + b], (i >> 1) & 1);
+      ok = ok && mbar_wait_warp(&m.bars[WB_READY + b], (i >> 1) & 1);
       if (!ok) break;
       fence_async_smem();
       tc_fence_after();
@@ -832,8 +833,8 @@ __device__ inline void wg_products2(const RoutedMaps& maps, int chunk, const Rou
       ok = wg_weights<NC, false>(maps, cfg, m, t, chunk, p);
       ++p;
       for (int at = lo; at < hi; at += 128, ++i) {
-        ok = ok && mbar_wait(&m.bars[WB_EFULL + er.s], er.ph);
-        if (i >= NBU) ok = ok && mbar_wait(&m.bars[WB_USED + u.s], u.ph ^ 1);
+        ok = ok && mbar_wait_warp(&m.bars[WB_EFULL + er.s], er.ph);
+        if (i >= NBU) ok = ok && mbar_wait_warp(&m.bars[WB_USED + u.s], u.ph ^ 1);
         if (!ok) break;
         fence_async_smem();
         tc_fence_after();
@@ -858,14 +859,14 @@ __device__ inline void wg_products2(const RoutedMaps& maps, int chunk, const Rou
   for (int t = 0; t < a.plan.T && ok; ++t) {
     int lo, hi;
     if (!wg_piece(m.spans, tile0, tile1, t, lo, hi)) continue;
-    if (p > 0) ok = mbar_wait(&m.bars[WB_ACCFREE], (p - 1) & 1);
+    if (p > 0) ok = mbar_wait_warp(&m.bars[WB_ACCFREE], (p - 1) & 1);
     ++p;
     for (int at = lo; at < hi; at += 128, ++i) {
-      ok = ok && mbar_wait(&m.bars[WB_READY + u.s], u.ph);
+      ok = ok && mbar_wait_warp(&m.bars[WB_READY + u.s], u.ph);
       if (!ok) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        ok = ok && mbar_wait(&m.bars[WB_YFULL + y.s], y.ph);
+        ok = ok && mbar_wait_warp(&m.bars[WB_YFULL + y.s], y.ph);
         if (!ok) break;
         fence_async_smem();
         tc_fence_after();
@@ -1286,14 +1287,14 @@ __global__ void __launch_bounds__(kDevThreads, 1)
       const int t = span_type(spans, T, tile * 128);
       if (t != prev) {
         if (p > 0) mma_commit(w_empty);      // the last behaviour's products
-        ok = mbar_wait(w_full, p & 1);
+        ok = mbar_wait_warp(w_full, p & 1);
         prev = t;
         ++p;
       }
-      if (i >= 2) ok = ok && mbar_wait(&e_empty[i & 1], ((i >> 1) & 1) ^ 1);
+      if (i >= 2) ok = ok && mbar_wait_warp(&e_empty[i & 1], ((i >> 1) & 1) ^ 1);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        ok = ok && mbar_wait(&a_full[r.s], r.ph);
+        ok = ok && mbar_wait_warp(&a_full[r.s], r.ph);
         if (!ok) break;
         fence_async_smem();
         tc_fence_after();

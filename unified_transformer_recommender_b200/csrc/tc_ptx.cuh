@@ -52,6 +52,16 @@ __device__ inline bool mbar_wait_limited(uint64_t* bar, uint32_t parity, uint32_
 __device__ inline bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return mbar_wait_limited(bar, parity, kSpinLimit);
 }
+// The same by a whole warp, with one outcome for all lanes: when the limit is
+// reached some lanes can see the phase complete in a round that others do not
+// make any more, and a warp that went on with a part of its lanes would never
+// get past a full-mask warp instruction (elect.sync, shuffles).
+__device__ inline bool mbar_wait_warp_limited(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  return __all_sync(~0u, mbar_wait_limited(bar, parity, limit));
+}
+__device__ inline bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return mbar_wait_warp_limited(bar, parity, kSpinLimit);
+}
 
 // ------------------------------------------------------------------ TMA --
 __device__ inline void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1, int c2) {
