@@ -29,7 +29,8 @@
 extern "C" {
 #endif
 
-/* Which buffer onetrans_input_workspace_size() sizes. */
+/* Which buffer onetrans_input_workspace_size() sizes.  A buffer of that size
+ * also serves calls with fewer ids or events (of the same or a smaller L). */
 typedef enum {
   ONETRANS_OP_EMBEDDING_BACKWARD = 0, /* n = R ids,    L = width */
   ONETRANS_OP_ROUTE = 1,              /* the plan: n = R events, L = k */

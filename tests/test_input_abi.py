@@ -36,6 +36,30 @@ def test_embedding_workspace():
     assert ot.lib.onetrans_input_workspace_size(None, 0, 1, 1, ctypes.byref(ot.SZ(0))) == ot.ERR_INVALID_ARG
 
 
+def test_a_workspace_serves_every_smaller_call():
+    """Sizes never fall as ids, events, width or choices grow: the sizes on both sides of every rule that picks larger
+    tiles or chunks, and of the numbers between, each against the largest before it."""
+    fm = FakeModel(n_beh=3, event_dim=64)
+    ends = [37_888, 81_920, 327_680, (1 << 20) - 1] + [i << 20 for i in range(1, 65)]
+    ns = sorted({n for e in ends for n in (e - 1, e, e + 1, e + 3000) if n <= 1 << 26} | {1, 31, 4096, 4097, 40_000, 400_000})
+    for w in (1, 8, 64, 256, 5000):
+        most = 0
+        for n in ns:
+            st, b = size_of(fm, ot.OP_EMBEDDING_BACKWARD, n, w)
+            assert st == ot.OK and b >= most, (n, w, b, most)
+            most = b
+    for n in ns:
+        sizes = [size_of(fm, ot.OP_EMBEDDING_BACKWARD, n, w)[1] for w in (1, 8, 64, 256, 5000)]
+        assert sizes == sorted(sizes)
+    for op in (ot.OP_ROUTE, ot.OP_ROUTED, ot.OP_ROUTED_BACKWARD):
+        for k in (1, 2, 8):
+            sizes = [size_of(fm, op, n, k)[1] for n in ns if n * k <= 1 << 26]
+            assert sizes == sorted(sizes), (op, k)
+        for n in (1, 1000, 40_000):
+            sizes = [size_of(fm, op, n, k)[1] for k in range(1, 9)]
+            assert sizes == sorted(sizes), (op, n)
+
+
 def test_lookup_argument_errors():
     fm = FakeModel()
     base = dict(m=fm.h, table=FAKE, tm=ot.BF16, V=100, w=64, ids=FAKE, bits=32, R=8, out=FAKE, ld=64)

@@ -65,6 +65,29 @@ struct EmbGrad {
 // 191, 3 million 488 / 468.
 static int sort_items(long long R) { return R <= 80 * 1024 ? 2 : R < 1 << 20 ? 4 : 8; }
 
+// Sorted positions a warp: 8 while that leaves all CTAs resident at once (4 an
+// SM), then more as the joins of the chunks would cost (whole gradient, rows
+// of 64: 1024 ids 8 / 32 positions 9.8 / 13.8 us, 75392 ids 8 / 16 33.8 / 31.4,
+// 524288 ids 16 / 32 132 / 120); at most 4096 chunks
+static int warp_rows(long long R) {
+  return R <= 148 * 4 * 8 * kRedWarps ? 8 : R <= 320 * 1024 ? 16 : 32 * (int)cdiv(R, 1 << 20);
+}
+
+// The last R, in no order, before one of the two rules above steps up.  With
+// the step come fewer tiles or chunks and so a smaller workspace: a buffer that
+// has to serve every call of up to n ids is sized for n and for each of these
+// below n.
+static const int kGradRuleEnds = 3 + (int)(kMaxGradIds >> 20);
+static long long grad_rule_end(int i) {
+  switch (i) {
+    case 0: return 148 * 4 * 8 * kRedWarps;
+    case 1: return 80 * 1024;
+    case 2: return 320 * 1024;
+    case 3: return (1 << 20) - 1;
+    default: return (long long)(i - 3) << 20;
+  }
+}
+
 static int key_bits(long long n_rows) {
   int b = 1;
   while ((n_rows >> b) != 0) ++b;
@@ -103,12 +126,7 @@ static onetrans_status emb_grad_impl(const EmbGrad& g, void* ws, size_t ws_bytes
   const long long R = g.R;
   const int items = sort_items(R), tile = kSortThreads * items;
   const int tiles = (int)cdiv(R, tile);
-  // sorted positions a warp: 8 while that leaves all CTAs resident at once (4 an
-  // SM), then more as the joins of the chunks would cost (whole gradient, rows
-  // of 64: 1024 ids 8 / 32 positions 9.8 / 13.8 us, 75392 ids 8 / 16 33.8 / 31.4,
-  // 524288 ids 16 / 32 132 / 120); at most 4096 chunks
-  const int wrows = R <= 148 * 4 * 8 * kRedWarps ? 8 : R <= 320 * 1024 ? 16 : 32 * (int)cdiv(R, 1 << 20);
-  const int chunk = kRedWarps * wrows;
+  const int chunk = kRedWarps * warp_rows(R);
   const int chunks = (int)cdiv(R, chunk);
   Carve cv(ws, ws_bytes);
   uint32_t* keys[2];
@@ -604,7 +622,15 @@ onetrans_status onetrans_input_workspace_size(const onetrans_model* m, int32_t o
       std::memset(&g, 0, sizeof(g));
       g.R = n;
       g.width = L;
-      return emb_grad_impl<int32_t>(g, nullptr, 0, nullptr, bytes);
+      OT_TRY(emb_grad_impl<int32_t>(g, nullptr, 0, nullptr, bytes));
+      for (int i = 0; i < kGradRuleEnds; ++i) {   // and whatever a call of fewer ids takes
+        size_t need = 0;
+        g.R = grad_rule_end(i);
+        if (g.R >= n) continue;
+        OT_TRY(emb_grad_impl<int32_t>(g, nullptr, 0, nullptr, &need));
+        *bytes = std::max(*bytes, need);
+      }
+      return ONETRANS_OK;
     }
     case ONETRANS_OP_ROUTE:
       OT_TRY(routed_check(m, n, L));
