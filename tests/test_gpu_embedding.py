@@ -306,3 +306,47 @@ def test_finite_differences():
         ref = float((dtable.double() * v.double()).sum())
         size = float((c.double().abs() * 1.5 * (table.abs() + v.abs())[ids.clamp(min=0).long()].double()).sum())
         assert abs(diff - ref) <= size * 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("R,V", [(1500, 100), (2500, 256), (9_000, 255), (300_000, 257), (300_000, 1000), (1_100_000, 3)])
+def test_zero_rows_among_popular_ids(R, V):
+    """Tables much smaller than R in which two rows of three are named by no id: many repeats of the ids on either
+    side of a row that has to be zero, in spans of 256 rows with few and with many ids."""
+    m, w = model("fp32"), 8
+    ids = make_ids("uniform", R, V, R + 41)
+    ids = torch.where(ids % 3 == 1, ids, torch.full_like(ids, -1)) if V > 3 else torch.where(ids >= 0, 1, ids).int()
+    dout = torch.randn(R, w, device="cuda")
+    dtable = torch.full((V, w), float("nan"), device="cuda")
+    ot.onetrans_embedding_backward(m, dout, ids, dtable, m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w), scale=0.5)
+    s, mag, n = reference(dout, ids, V, 0.5)
+    assert (n > 0).sum() <= V // 3 + 1
+    check_rows(dtable, s, mag, n)
+    assert (dtable[n == 0] == 0).all()
+    assert ot.onetrans_device_status() == 0
+
+
+def test_dense_gradient_into_a_small_table_takes_about_the_sparse_ones_time():
+    """The dense form does what the sparse one does and writes the rows that no id names.  With 2^22 ids of 256 rows
+    there are none, so finding that out must not cost more than the sums did (it once took one CTA's walk over all
+    ids: 17 times the sparse form's time)."""
+    m, R, V, w = model("bf16"), 1 << 22, 256, 16
+    dout, ids = torch.randn(R, w, device="cuda").bfloat16(), make_ids("uniform", R, V, 47)
+    ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w)
+    dtable, rows = torch.empty(V, w, device="cuda"), torch.empty(V, w, device="cuda")
+    uniq, n = torch.empty(V, device="cuda", dtype=torch.int32), torch.empty(1, device="cuda", dtype=torch.int32)
+
+    def best(f):
+        t = []
+        for _ in range(7):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            f()
+            e1.record()
+            e1.synchronize()
+            t.append(e0.elapsed_time(e1))
+        return min(t)
+
+    dense = best(lambda: ot.onetrans_embedding_backward(m, dout, ids, dtable, ws))
+    sparse = best(lambda: ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, rows, n, ws))
+    assert torch.equal(rows[:int(n.item())], dtable[:int(n.item())])
+    assert dense <= 2 * sparse, (dense, sparse)

@@ -501,9 +501,17 @@ __device__ inline long long emb_lower_bound(const uint32_t* __restrict__ keys, l
   return lo;
 }
 
-// Zeros for the 256 table rows from v0 that no id names.
+// Zeros for the 256 table rows from v0 that no id names.  Which ones the sorted
+// ids between the rows' bounds say: a short span is walked, each position that
+// begins a run marking its row; in a long one (small tables, popular ids) each
+// thread searches for its own row, about 20 dependent loads whatever R.  Whole
+// dense gradient of 262144 ids, rows of 64, walk / search, us: 1024 ids a span
+// 59 / 66, 4096 53 / 57, 8192 57 / 57, 16384 63 / 56, 65536 103 / 55; of 2^22
+// ids of 256 rows of 16 (one span) 7600 / 480, the sums alone 450.
+constexpr int kFillWalk = 8192;    // ids of a span that is walked
 template <int CPL>
 __device__ inline void emb_fill_absent(const ReduceArgs& a, long long v0, int col) {
+  static_assert(32 * kRedWarps == 256, "a thread per row");
   __shared__ unsigned s_there[kRedWarps];
   __shared__ long long s_span[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -513,10 +521,21 @@ __device__ inline void emb_fill_absent(const ReduceArgs& a, long long v0, int co
     if (lane == 0) s_span[warp] = p;
   }
   __syncthreads();
-  // the ids between: each position that begins a run marks its row
-  for (long long p = s_span[0] + threadIdx.x; p < s_span[1]; p += 32 * kRedWarps) {
-    const uint32_t k = a.keys[p];
-    if (p == s_span[0] || a.keys[p - 1] != k) atomicOr(&s_there[(k - v0) >> 5], 1u << ((k - v0) & 31));
+  const long long s0 = s_span[0], s1 = s_span[1];
+  if (s1 - s0 <= kFillWalk) {
+    for (long long p = s0 + threadIdx.x; p < s1; p += 32 * kRedWarps) {
+      const uint32_t k = a.keys[p];
+      if (p == s0 || a.keys[p - 1] != k) atomicOr(&s_there[(k - v0) >> 5], 1u << ((k - v0) & 31));
+    }
+  } else {
+    const uint32_t v = (uint32_t)(v0 + threadIdx.x);
+    long long lo = s0, hi = s1;          // keys before lo are < v, keys from hi on are not
+    while (lo < hi) {
+      const long long mid = (lo + hi) >> 1;
+      if (a.keys[mid] < v) lo = mid + 1; else hi = mid;
+    }
+    const unsigned there = __ballot_sync(~0u, lo < s1 && a.keys[lo] == v);
+    if (lane == 0) s_there[warp] = there;
   }
   __syncthreads();
   if (col >= a.width) return;
