@@ -182,3 +182,18 @@ def test_routed_argument_errors():
     fp = FakeModel(n_beh=3, event_dim=64, mode=ot.FP32)
     keep[2][1] = FAKE
     assert grad(m=fp.h, dm=ot.BF16) == ot.ERR_UNSUPPORTED
+
+
+def test_rows_per_sample_past_the_events_is_one_sample():
+    """Any rows_per_sample of at least R means rows one after another, also one past 32 bits: such a call gets past the
+    checks of the token rows, here to the one of the workspace."""
+    fm = FakeModel(n_beh=3, event_dim=64)
+    d = fm.cfg.d_model
+    g, keep = event_grads(3)
+    plan = size_of(fm, ot.OP_ROUTE, 8, 2)[1]
+    for per in (8, 9, 2 ** 31 - 1, 2 ** 31, 2 ** 40, 2 ** 63 - 1):
+        assert ot.lib.onetrans_tokenize_routed(fm.h, FAKE, None, 8, 2, FAKE, plan, FAKE, per, 0, FAKE, 0, None) == ot.ERR_CAPACITY
+        assert ot.lib.onetrans_tokenize_routed_backward(fm.h, FAKE, None, 8, 2, FAKE, plan, FAKE, ot.FP32, per, 0, None, None,
+                                                        ctypes.byref(g), FAKE, 0, None) == ot.ERR_CAPACITY
+    for per in (0, -1, -2 ** 63):
+        assert ot.lib.onetrans_tokenize_routed(fm.h, FAKE, None, 8, 2, FAKE, plan, FAKE, per, 8 * d, FAKE, 0, None) == ot.ERR_SHAPE

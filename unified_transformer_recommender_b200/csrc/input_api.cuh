@@ -276,9 +276,13 @@ static onetrans_status routed_check(const onetrans_model* m, long long R, int k)
   if (!aligned(m->type_emb, 16)) return ONETRANS_ERR_INVALID_ARG;
   return ONETRANS_OK;
 }
+// With R <= per (any per) there is one sample and its stride is not looked at.
 static onetrans_status token_rows_check(const onetrans_model* m, long long R, long long per, long long sample_ld) {
-  if (per < 1 || per > 0x7fffffff || (R > per && sample_ld < per * m->d)) return ONETRANS_ERR_SHAPE;
+  if (per < 1 || (R > per && sample_ld < per * m->d)) return ONETRANS_ERR_SHAPE;
   return ONETRANS_OK;
+}
+static TokenRows token_rows(long long per, long long sample_ld) {
+  return TokenRows{(int)std::min(per, 0x7fffffffLL), sample_ld};
 }
 
 static RoutedMLP routed_mlp_of(const onetrans_model* m) {
@@ -721,7 +725,7 @@ onetrans_status onetrans_tokenize_routed(const onetrans_model* m, const void* ev
   std::memset(&c, 0, sizeof(c));
   c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
   c.tokens = tokens;
-  c.rows = TokenRows{(int)rows_per_sample, sample_ld};
+  c.rows = token_rows(rows_per_sample, sample_ld);
   return tokenize_routed_any(m, &c, R, k, ws, ws_bytes, (cudaStream_t)stream, nullptr);
 }
 
@@ -768,7 +772,7 @@ onetrans_status onetrans_tokenize_routed_backward(const onetrans_model* m, const
   if (ws_bytes < need) return ONETRANS_ERR_CAPACITY;
   c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
   c.dtokens = dtokens; c.dtokens_mode = dtokens_mode;
-  c.rows = TokenRows{(int)rows_per_sample, sample_ld};
+  c.rows = token_rows(rows_per_sample, sample_ld);
   c.devents = devents; c.dweights = dweights;
   return routed_backward_any(m, &c, R, k, ws, ws_bytes, st, nullptr);
 }
