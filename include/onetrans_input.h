@@ -106,7 +106,7 @@ ONETRANS_API onetrans_status onetrans_route_events(const onetrans_model* m, cons
  *     (r % rows_per_sample) * d elements, so that the S rows of x0
  *     [B, L_S + L_NS, d] are written in place (rows_per_sample = L_S,
  *     sample_ld = (L_S + L_NS) * d); rows_per_sample >= R: rows one after
- *     another.  Elements outside those rows are left as they were.
+ *     another, sample_ld is not looked at.  Elements outside those rows are left as they were.
  * A plan that onetrans_route_events did not make for this model's behaviours,
  * R and k sets the device status word (code 3) and nothing is written.
  * BF16 mode: the hidden row z is rounded to bf16 as the operand of the second

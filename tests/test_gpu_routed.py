@@ -561,3 +561,34 @@ def test_choice_weights_reach_every_sum_exactly(d, k):
                 assert (grads[f][t] == scale * n).all(), (seed, t, f)
             assert (grads["type_emb"][t] == n).all()
         assert (dw[types >= 0] == 16 * d).all() and (dw[types < 0] == 0).all() and (de == 0).all()
+
+
+@pytest.mark.parametrize("mode,d,k", [("bf16", 256, 1), ("bf16", 128, 2), ("fp32", 64, 2)])
+def test_the_stride_of_a_lone_sample_changes_nothing(mode, d, k):
+    """With rows_per_sample >= R the sample stride is unused: whatever it is, the same kernels run and give the same
+    bits, forward and backward (an odd one once sent a bf16 call to the CUDA-core kernels, which round less)."""
+    R, T, e = 333, 3, 64
+    m, W, ev, types, wt, plan, g = inputs(mode, R, T, k, e, d, True, "skewed")
+    ot.onetrans_route_events(m, types, plan)
+    ws, wsb = m.input_workspace(ot.OP_ROUTED, R, k), m.input_workspace(ot.OP_ROUTED_BACKWARD, R, k)
+    st = torch.cuda.current_stream().cuda_stream
+    dy = torch.randn(R, d, device="cuda", generator=g)
+    out = []
+    for per, ld in ((R, R * d), (R, 0), (R, 1), (R + 1, 12_345), (2 ** 40, -7)):
+        tok = torch.empty(R, d, device="cuda", dtype=DT[mode])
+        ot._check("tokens", ot.lib.onetrans_tokenize_routed(m.handle, ev.data_ptr(), wt.data_ptr(), R, k, plan.data_ptr(),
+                                                            plan.numel(), tok.data_ptr(), per, ld, ws.data_ptr(), ws.numel(), st))
+        grads = {f: [torch.empty(tuple(x.shape), device="cuda") for x in W[f]] for f in ("Wb1", "bb1", "Wb2", "bb2")}
+        emb, de, dw = torch.empty(T, d, device="cuda"), torch.empty_like(ev), torch.empty(R, k, device="cuda")
+        s, keep = ot.EventGrads(), []
+        for f in ("Wb1", "bb1", "Wb2", "bb2"):
+            keep.append((ot.P * T)(*[x.data_ptr() for x in grads[f]]))
+            setattr(s, f, ot.ctypes.cast(keep[-1], ot.PP))
+        s.type_emb = emb.data_ptr()
+        ot._check("gradient", ot.lib.onetrans_tokenize_routed_backward(
+            m.handle, ev.data_ptr(), wt.data_ptr(), R, k, plan.data_ptr(), plan.numel(), dy.data_ptr(), ot.FP32, per, ld,
+            de.data_ptr(), dw.data_ptr(), ot.ctypes.byref(s), wsb.data_ptr(), wsb.numel(), st))
+        out.append([tok, de, dw, emb] + [x for f in ("Wb1", "bb1", "Wb2", "bb2") for x in grads[f]])
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0], other))
+    assert ot.onetrans_device_status() == 0

@@ -281,8 +281,10 @@ static onetrans_status token_rows_check(const onetrans_model* m, long long R, lo
   if (per < 1 || (R > per && sample_ld < per * m->d)) return ONETRANS_ERR_SHAPE;
   return ONETRANS_OK;
 }
-static TokenRows token_rows(long long per, long long sample_ld) {
-  return TokenRows{(int)std::min(per, 0x7fffffffLL), sample_ld};
+// The stride of a lone sample is 0 from here on, so that no choice of kernels
+// or accesses depends on it.
+static TokenRows token_rows(long long R, long long per, long long sample_ld) {
+  return R <= per ? TokenRows{0x7fffffff, 0} : TokenRows{(int)per, sample_ld};
 }
 
 static RoutedMLP routed_mlp_of(const onetrans_model* m) {
@@ -725,7 +727,7 @@ onetrans_status onetrans_tokenize_routed(const onetrans_model* m, const void* ev
   std::memset(&c, 0, sizeof(c));
   c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
   c.tokens = tokens;
-  c.rows = token_rows(rows_per_sample, sample_ld);
+  c.rows = token_rows(R, rows_per_sample, sample_ld);
   return tokenize_routed_any(m, &c, R, k, ws, ws_bytes, (cudaStream_t)stream, nullptr);
 }
 
@@ -772,7 +774,7 @@ onetrans_status onetrans_tokenize_routed_backward(const onetrans_model* m, const
   if (ws_bytes < need) return ONETRANS_ERR_CAPACITY;
   c.events = events; c.weights = weights; c.R = R; c.k = k; c.plan = &p;
   c.dtokens = dtokens; c.dtokens_mode = dtokens_mode;
-  c.rows = token_rows(rows_per_sample, sample_ld);
+  c.rows = token_rows(R, rows_per_sample, sample_ld);
   c.devents = devents; c.dweights = dweights;
   return routed_backward_any(m, &c, R, k, ws, ws_bytes, st, nullptr);
 }
