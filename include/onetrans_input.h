@@ -50,8 +50,8 @@ ONETRANS_API onetrans_status onetrans_input_workspace_size(const onetrans_model*
 /* out[r] = scale * table[ids[r]] (a zero row for padding), R rows.
  *   table [n_rows, width] of element type table_mode (ONETRANS_BF16 or
  *   ONETRANS_FP32); out: rows of the mode's type, out_ld >= width elements
- *   apart (so that the fields of one feature row can be looked up side by
- *   side); what lies between two rows is left as it was.  The product is
+ *   apart, 4-byte aligned (so that the fields of one feature row can be
+ *   looked up side by side); what lies between two rows is left as it was.  The product is
  *   taken in float32 and rounded once. */
 ONETRANS_API onetrans_status onetrans_embedding_lookup(const onetrans_model* m, const void* table,
                                                        int32_t table_mode, int64_t n_rows, int32_t width,

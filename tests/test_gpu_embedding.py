@@ -350,3 +350,37 @@ def test_dense_gradient_into_a_small_table_takes_about_the_sparse_ones_time():
     sparse = best(lambda: ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, rows, n, ws))
     assert torch.equal(rows[:int(n.item())], dtable[:int(n.item())])
     assert dense <= 2 * sparse, (dense, sparse)
+
+
+# fields of one feature row, side by side: widths, the first one's column
+FIELDS = [("bf16", (50, 14, 6, 64, 2), 0), ("bf16", (8, 16, 24), 4), ("fp32", (50, 7, 1, 3, 64), 0), ("fp32", (4, 8), 1)]
+
+
+@pytest.mark.parametrize("mode,widths,first", FIELDS)
+@pytest.mark.parametrize("R", [300, 40_000])
+def test_fields_of_a_feature_row_are_looked_up_side_by_side(mode, widths, first, R):
+    """Each field's rows go to its columns of one wide row, whose starts are 4-byte aligned and no more."""
+    m = model(mode)
+    total = first + sum(widths) + 4
+    row = torch.full((R, total), 7.0, device="cuda", dtype=DT[mode])
+    want = row.double()
+    col = first
+    for i, w in enumerate(widths):
+        for table_t in ("bf16", "fp32"):          # the last one stays
+            V = 40 + i
+            table, ids = torch.randn(V, w, device="cuda").to(DT[table_t]), make_ids("uniform", R, V, 50 + i)
+            ot.onetrans_embedding_lookup(m, table, ids, row[:, col:col + w], scale=2.0)
+        want[:, col:col + w] = torch.where((ids >= 0)[:, None], table[ids.clamp(min=0).long()].double() * 2.0, 0.0)
+        col += w
+    err = (row.double() - want).abs()
+    assert (err <= want.abs() * HALF[mode]).all()             # the product by 2 is exact
+    assert (row[:, :first] == 7.0).all() and (row[:, col:] == 7.0).all()
+    assert ot.onetrans_device_status() == 0
+
+
+def test_a_field_at_an_odd_bf16_column_is_refused():
+    row = torch.zeros(10, 20, device="cuda", dtype=torch.bfloat16)
+    ids = torch.zeros(10, device="cuda", dtype=torch.int32)
+    with pytest.raises(ot.OneTransError) as e:
+        ot.onetrans_embedding_lookup(model("bf16"), torch.zeros(5, 8, device="cuda"), ids, row[:, 3:11])
+    assert e.value.status == ot.ERR_INVALID_ARG

@@ -491,7 +491,8 @@ def _rows(t: torch.Tensor, what: str):
 def onetrans_embedding_lookup(model: Model, table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor,
                               scale: float = 1.0, stream=None) -> None:
     """out[r] = scale * table[ids[r]]; id -1 gives a zero row.  table [V, w] bf16 or float32; ids [R] int32 or
-    int64; out [R, w] of the model dtype, rows contiguous, any row stride."""
+    int64; out [R, w] of the model dtype, rows contiguous, any row stride, 4-byte aligned (columns of a wider
+    feature row: any column in float32, an even one in bf16)."""
     _on_one_device(table, ids, out)
     R, ld, w = _rows(out, "out")
     tm, bits, ts = _MODE_OF.get(table.dtype), _ID_BITS.get(ids.dtype), table.shape

@@ -14,15 +14,20 @@ static bool allow_smem(K kernel, size_t bytes) {
 static const long long kMaxTableRows = 0x7fffffff, kMaxGradIds = 1LL << 26;
 static const int kMaxWidth = 65536;
 
+// Whether groups of n elements that start at p and at multiples of n elements
+// after it can be accessed as vectors of 16 bytes at most.
+static bool vec_at(const void* p, int n, size_t elem) { return aligned(p, std::min<size_t>(n * elem, 16)); }
+
 static bool mode_ok(int32_t mode) { return mode == ONETRANS_BF16 || mode == ONETRANS_FP32; }
 
 // ----------------------------------------------------------------- lookup --
 template <typename Tt, typename To, typename Id>
 static onetrans_status lookup_impl(const void* table, long long n_rows, int width, const void* ids, long long R,
                                    float scale, void* out, long long out_ld, cudaStream_t st) {
-  // 16 bytes of the narrower type's row per access where the rows keep that alignment
+  // 16 bytes of the narrower type's row per access where the rows keep that
+  // alignment (a field inside a wider row may start at any 4 bytes)
   int ve = sizeof(Tt) == 4 && sizeof(To) == 4 ? 4 : 8;
-  while (width % ve || out_ld % ve) ve >>= 1;
+  while (width % ve || out_ld % ve || !vec_at(out, ve, sizeof(To))) ve >>= 1;
   const int groups = width / ve, cpr = std::min(groups, kLookThreads), rpb = kLookThreads / cpr;
   // four rows in flight per thread once that still gives every SM two CTAs
   // (rows of 64 bf16, one row against four: 8192 2.1 / 2.3 us, 65536 4.3 / 4.0,
@@ -661,7 +666,7 @@ onetrans_status onetrans_embedding_lookup(const onetrans_model* m, const void* t
       out_ld < width)
     return ONETRANS_ERR_SHAPE;
   if (R == 0) return ONETRANS_OK;
-  if (!table || !ids || !out || !aligned(table, 16) || !aligned(ids, 16) || !aligned(out, 16))
+  if (!table || !ids || !out || !aligned(table, 16) || !aligned(ids, 16) || !aligned(out, 4))
     return ONETRANS_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const bool tb = table_mode == ONETRANS_BF16, w = ids_bits == 64;
