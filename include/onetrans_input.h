@@ -61,7 +61,8 @@ ONETRANS_API onetrans_status onetrans_embedding_lookup(const onetrans_model* m, 
 /* The gradient of a lookup, dense: dtable[v] = scale * (sum of dout[r] over
  * the r with ids[r] = v), float32, every row of dtable [n_rows, width]
  * written (zeros where no id names it).
- *   dout: rows of element type dout_mode, dout_ld >= width elements apart.
+ *   dout: rows of element type dout_mode, dout_ld >= width elements apart,
+ *     4-byte aligned (the columns of one field of a wider gradient).
  * R = 0 still writes the zeros.  R <= 2^26.  Workspace:
  * ONETRANS_OP_EMBEDDING_BACKWARD. */
 ONETRANS_API onetrans_status onetrans_embedding_backward(const onetrans_model* m, const void* dout,

@@ -384,3 +384,34 @@ def test_a_field_at_an_odd_bf16_column_is_refused():
     with pytest.raises(ot.OneTransError) as e:
         ot.onetrans_embedding_lookup(model("bf16"), torch.zeros(5, 8, device="cuda"), ids, row[:, 3:11])
     assert e.value.status == ot.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dout_t,widths,first", FIELDS)
+@pytest.mark.parametrize("R", [300, 40_000])
+def test_gradients_of_the_fields_of_a_feature_row(dout_t, widths, first, R):
+    """Each field's gradient is read from its columns of the wide row's gradient, whose starts are 4-byte aligned."""
+    m = model("bf16")
+    row = torch.randn(R, first + sum(widths) + 4, device="cuda").to(DT[dout_t])
+    col = first
+    for i, w in enumerate(widths):
+        V = 40 + i
+        dout, ids = row[:, col:col + w], make_ids("popular", R, V, 60 + i)
+        ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w)
+        dtable, rows = torch.full((V, w), float("nan"), device="cuda"), torch.full((V, w), float("nan"), device="cuda")
+        uniq, n = torch.empty(V, device="cuda", dtype=torch.int32), torch.empty(1, device="cuda", dtype=torch.int32)
+        ot.onetrans_embedding_backward(m, dout, ids, dtable, ws, scale=0.75)
+        ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, rows, n, ws, scale=0.75)
+        s, mag, cnt = reference(dout, ids, V, 0.75)
+        check_rows(dtable, s, mag, cnt)
+        assert torch.equal(rows[:int(n.item())], dtable[cnt > 0])
+        col += w
+    assert ot.onetrans_device_status() == 0
+
+
+def test_a_gradient_field_at_an_odd_bf16_column_is_refused():
+    row = torch.zeros(10, 20, device="cuda", dtype=torch.bfloat16)
+    ids, m = torch.zeros(10, device="cuda", dtype=torch.int32), model("bf16")
+    with pytest.raises(ot.OneTransError) as e:
+        ot.onetrans_embedding_backward(m, row[:, 3:11], ids, torch.zeros(5, 8, device="cuda"),
+                                       m.input_workspace(ot.OP_EMBEDDING_BACKWARD, 10, 8))
+    assert e.value.status == ot.ERR_INVALID_ARG

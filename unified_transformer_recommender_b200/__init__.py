@@ -519,7 +519,7 @@ def _grad_args(dout: torch.Tensor, ids: torch.Tensor):
 def onetrans_embedding_backward(model: Model, dout: torch.Tensor, ids: torch.Tensor, dtable: torch.Tensor,
                                 ws: torch.Tensor, scale: float = 1.0, stream=None) -> None:
     """dtable[v] = scale * sum of dout[r] over ids[r] = v, every row of dtable [V, w] float32 written.  dout
-    [R, w] bf16 or float32, rows contiguous, any row stride."""
+    [R, w] bf16 or float32, rows contiguous, any row stride, 4-byte aligned (columns of a wider gradient)."""
     _on_one_device(dout, ids, dtable, ws)
     ld, w = _grad_args(dout, ids)
     _need(dtable.dim() == 2 and dtable.is_contiguous() and dtable.dtype == torch.float32 and dtable.shape[1] == w,

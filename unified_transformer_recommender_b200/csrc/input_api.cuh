@@ -109,7 +109,7 @@ template <typename T, typename Id, bool DENSE>
 static onetrans_status emb_reduce_launch(const EmbGrad& g, ReduceArgs a, cudaStream_t st) {
   int cpl = 1;
   while (cpl < 8 && 32 * cpl < g.width) cpl *= 2;
-  while (g.width % cpl || g.dout_ld % cpl) cpl >>= 1;
+  while (g.width % cpl || g.dout_ld % cpl || !vec_at(g.dout, cpl, sizeof(T))) cpl >>= 1;
   a.fill = DENSE ? (int)cdiv(g.n_rows, 256) : 0;
   const dim3 grid((unsigned)(a.chunks + a.fill), (unsigned)cdiv(g.width, 32 * cpl));
   const dim3 jgrid((unsigned)a.chunks, grid.y);
@@ -228,7 +228,7 @@ static onetrans_status emb_grad_check(const onetrans_model* m, const EmbGrad& g)
 }
 
 static onetrans_status emb_grad_run(const EmbGrad& g, void* ws, size_t ws_bytes, cudaStream_t st) {
-  if (g.R > 0 && (!g.dout || !g.ids || !ws || !aligned(g.dout, 16) || !aligned(g.ids, 16) || !aligned(ws, 256)))
+  if (g.R > 0 && (!g.dout || !g.ids || !ws || !aligned(g.dout, 4) || !aligned(g.ids, 16) || !aligned(ws, 256)))
     return ONETRANS_ERR_INVALID_ARG;
   return g.ids_bits == 32 ? emb_grad_impl<int32_t>(g, ws, ws_bytes, st, nullptr)
                           : emb_grad_impl<int64_t>(g, ws, ws_bytes, st, nullptr);
