@@ -592,3 +592,41 @@ def test_the_stride_of_a_lone_sample_changes_nothing(mode, d, k):
     for other in out[1:]:
         assert all(torch.equal(a, b) for a, b in zip(out[0], other))
     assert ot.onetrans_device_status() == 0
+
+
+@pytest.mark.parametrize("mode,d,e", [("fp32", 64, 24), ("bf16", 96, 20), ("bf16", 128, 64)])
+def test_hidden_units_whose_squares_overflow_keep_a_finite_slope(mode, d, e):
+    """Events of 1e19 and more give u whose square is past float32: GELU's slope there is 0 or 1, and the event's
+    gradient W1^T (w dz slope) an ordinary number (the polynomial factor of the slope, inf, times its 0 once made NaN).
+    Off by the float32 sums, in bf16 mode by du's and the event gradient's roundings (2^-8 each)."""
+    T, R = 2, 200
+    m, W = make(mode, T, e, d, 121)
+    g = torch.Generator(device="cuda").manual_seed(122)
+    ev = torch.randn(R, e, device="cuda", generator=g)
+    ev[::3] *= 2.0 ** 66
+    ev = ev.to(DT[mode])
+    types = make_types("uniform", R, 1, T, 123)
+    wt, dy = torch.rand(R, 1, device="cuda", generator=g) + 0.5, torch.randn(R, d, device="cuda", generator=g).to(DT[mode])
+    plan = m.input_workspace(ot.OP_ROUTE, R, 1)
+    ot.onetrans_route_events(m, types, plan)
+    de, dw = torch.empty_like(ev), torch.empty(R, 1, device="cuda")
+    grads = {f: [torch.empty(tuple(x.shape), device="cuda") for x in W[f]] for f in ("Wb1", "bb1", "Wb2", "bb2")}
+    grads["type_emb"] = torch.empty(T, d, device="cuda")
+    ot.onetrans_tokenize_routed_backward(m, ev, types, wt, plan, dy, de, dw, grads, m.input_workspace(ot.OP_ROUTED_BACKWARD, R, 1))
+    assert ot.onetrans_device_status() == 0
+    for f in grads:
+        assert all(torch.isfinite(x).all() for x in grads[f]), f
+    assert torch.isfinite(dw).all()
+    u23, one = 2.0 ** -23, 2.0 ** -8 * 1.01 if mode == "bf16" else 2.0 ** -24
+    big = torch.arange(R, device="cuda") % 3 == 0
+    for t in range(T):
+        r = torch.nonzero((types[:, 0] == t) & big)[:, 0]
+        W1, W2 = W["Wb1"][t].double(), W["Wb2"][t].double()
+        u, _, slope = parts(W, t, ev[r].double())
+        assert (u.abs() > 1e10).all() and ((slope == 0) | (slope == 1)).all()
+        y = dy[r].double()
+        du = wt[r].double() * (y @ W2) * slope
+        edu = wt[r].double() * (y.abs() @ W2.abs()) * ((d + 2) * u23) + du.abs() * (one + 4 * u23)
+        ref = du @ W1
+        tol = edu @ W1.abs() + (du.abs() @ W1.abs()) * ((2 * d + 2) * u23)
+        close(de[r], ref, tol + (ref.abs() + tol) * one, "devents")

@@ -192,12 +192,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const int* _
 }
 
 // ----------------------------------------------------- CUDA-core products --
-// GELU-tanh and its slope in float32 (accurate tanh).
+// GELU-tanh and its slope in float32 (accurate tanh).  u^2 is bounded in the
+// slope: past |u| = 16 its factor 1 - th^2 is 0, and inf * 0 would follow.
 __device__ inline void gelu_and_slope(float u, float& z, float& g) {
   const float c = 0.7978845608028654f, a = 0.044715f;
   const float th = tanhf(c * (u + a * u * u * u));
   z = 0.5f * u * (1.f + th);
-  g = 0.5f * (1.f + th) + 0.5f * u * (1.f - th * th) * c * (1.f + 3.f * a * u * u);
+  g = 0.5f * (1.f + th) + 0.5f * u * (1.f - th * th) * c * (1.f + 3.f * a * fminf(u * u, 256.f));
 }
 
 // An upstream gradient as a matrix operand: of the mode's type, also where the
