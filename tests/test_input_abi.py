@@ -5,6 +5,9 @@ import ctypes
 import os
 import re
 
+import pytest
+import torch
+
 import unified_transformer_recommender_b200 as ot
 from test_host_abi import FAKE, FakeModel
 
@@ -197,3 +200,21 @@ def test_rows_per_sample_past_the_events_is_one_sample():
                                                         ctypes.byref(g), FAKE, 0, None) == ot.ERR_CAPACITY
     for per in (0, -1, -2 ** 63):
         assert ot.lib.onetrans_tokenize_routed(fm.h, FAKE, None, 8, 2, FAKE, plan, FAKE, per, 8 * d, FAKE, 0, None) == ot.ERR_SHAPE
+
+
+def test_a_model_on_another_device_is_refused(monkeypatch):
+    """The kernels of a routed call run on the current device and read the model's weights there.  Without a second
+    device here, the current one is said to be the one the arguments are on, and the weights' another."""
+    from onetrans_synth import ModelShape, make_weights
+    sh = ModelShape(n_layers=1, d=64, n_heads=1, d_ff=64, L_NS=2, ns_feat=16, ns_hidden=64, behavior_dims=(64, 64))
+    m = ot.model_from_arrays(sh, make_weights(sh, 1, "bf16"), device="cpu", event_dim=64)
+    ev, tok = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.bfloat16)
+    types, ws = torch.zeros(4, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    dev = ev.get_device()
+    assert m.device_index == dev
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: dev)
+    m.device_index = dev + 2
+    for call in (lambda: ot.onetrans_tokenize_routed(m, ev, types, None, ws, tok, ws),
+                 lambda: ot.onetrans_tokenize_routed_backward(m, ev, types, None, ws, tok, None, None, {"type_emb": tok}, ws)):
+        with pytest.raises(ValueError, match="the model's weights must be on the current CUDA device"):
+            call()

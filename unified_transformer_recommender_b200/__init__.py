@@ -215,6 +215,7 @@ class Model:
                  ns_feat_dim: int = 0, ns_hidden: int = 0, n_behaviors: int = 0,
                  event_dim: int = 0, rms_eps: float = 1e-6, page_tokens: int = 64):
         self._keep = []
+        self.device_index = None     # of the weights' device (-1: the CPU)
         self.dtype = torch.bfloat16 if mode == BF16 else torch.float32
         self._pyr = _i32(pyramid_q) if pyramid_q is not None else None
         self.cfg = Config(n_layers, d_model, n_heads, d_ff, L_NS, ns_feat_dim, ns_hidden,
@@ -245,6 +246,7 @@ class Model:
     def _own(self, t: torch.Tensor) -> torch.Tensor:
         if t.dtype != self.dtype or not t.is_contiguous():
             raise ValueError("weights must be contiguous tensors of the model dtype")
+        self.device_index = t.get_device()
         self._keep.append(t)
         return t
 
@@ -569,6 +571,8 @@ def _token_rows(t: torch.Tensor, R: int, d: int, what: str):
 
 def _routed_args(model: Model, events, types, weights, plan, ws, *more):
     _on_one_device(events, types, weights, plan, ws, *more)
+    if model.device_index != torch.cuda.current_device():
+        raise ValueError(f"the model's weights must be on the current CUDA device ({torch.cuda.current_device()})")
     R, k = _choices(types)
     e = model.cfg.event_dim
     _need(events.dim() == 2 and tuple(events.shape) == (R, e) and events.is_contiguous() and events.dtype == model.dtype,
