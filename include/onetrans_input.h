@@ -137,7 +137,9 @@ typedef struct {
  * BF16 mode: float32 dtokens are rounded to bf16 as matrix operands; z and
  * the pre-activation gradient enter the weight gradients' products as two
  * bf16 terms (16 bits of significand), and the event gradient's product as
- * one, rounded once more as devents are stored.  R = 0 writes the zeros of
+ * one, rounded once more as devents are stored (two terms of either sign times
+ * an infinity: an infinite dtokens or events element makes NaN of its
+ * behaviour's weight gradients).  R = 0 writes the zeros of
  * grads.  The plan is checked as above. */
 ONETRANS_API onetrans_status onetrans_tokenize_routed_backward(
     const onetrans_model* m, const void* events, const float* weights, int64_t R, int32_t k, const void* plan,

@@ -630,3 +630,35 @@ def test_hidden_units_whose_squares_overflow_keep_a_finite_slope(mode, d, e):
         ref = du @ W1
         tol = edu @ W1.abs() + (du.abs() @ W1.abs()) * ((2 * d + 2) * u23)
         close(de[r], ref, tol + (ref.abs() + tol) * one, "devents")
+
+
+@pytest.mark.parametrize("R,T,k,e,d", [(30_000, 3, 1, 64, 256), (20_011, 8, 2, 64, 384)])
+def test_weight_gradients_of_many_events_norm_wise(R, T, k, e, d):
+    """The element bounds above grow with the number of events, past what a lost low term of z or du would cost; the
+    norm does not.  dtokens are random and independent of z, so the terms of a sum and their errors both add up as
+    random walks: the two bf16 terms' rounding (2^-16 at most, 2^-16.8 in the mean square), and the tensor cores'
+    truncated float32 sums (about 126 additions of a piece, 2^-24 each in the mean, all of one sign: 2^-17) make about
+    2^-15.5 of the norm.  The bar is 2^-12.  With one term (2^-8 at most, 2^-9.3 in the mean square) the oracle itself
+    is twice past it and more."""
+    m, W, ev, types, wt, plan, g = inputs("bf16", R, T, k, e, d, True, "skewed")
+    dy = torch.randn(R, d, device="cuda", generator=g).bfloat16()
+    ot.onetrans_route_events(m, types, plan)
+    grads = {f: [torch.empty(tuple(x.shape), device="cuda") for x in W[f]] for f in ("Wb1", "bb1", "Wb2", "bb2")}
+    grads["type_emb"] = torch.empty(T, d, device="cuda")
+    ot.onetrans_tokenize_routed_backward(m, ev, types, wt, plan, dy, None, None, grads, m.input_workspace(ot.OP_ROUTED_BACKWARD, R, k))
+    assert ot.onetrans_device_status() == 0
+    ref, _ = backward_ref(W, ev, types, wt, dy, dy, "bf16")
+
+    def off(got, want):
+        return float((got.double() - want).norm() / want.norm())
+
+    for f in ("Wb1", "bb1", "Wb2", "bb2"):
+        for t in range(T):
+            assert off(grads[f][t], ref[f][t]) <= 2.0 ** -12, (f, t)
+    Wc = {f: ([x.cpu() for x in W[f]] if isinstance(W[f], list) else W[f].cpu()) for f in W}   # the planted mistake
+    r = torch.nonzero(types[:, 0].cpu() == 0)[:, 0]
+    x, w, y = ev.cpu()[r].double(), wt.cpu()[r, 0].double()[:, None], dy.cpu()[r].double()
+    _, z, slope = parts(Wc, 0, x)
+    z, du = w * z, w * (y @ Wc["Wb2"][0].double()) * slope
+    assert off(y.t() @ z.bfloat16().double(), y.t() @ z) > 2.0 ** -11
+    assert off(du.bfloat16().double().t() @ x, du.t() @ x) > 2.0 ** -11
