@@ -101,9 +101,11 @@ static int key_bits(long long n_rows) {
 
 // Tiles whose counts every CTA of a pass adds up itself (it reads tiles x
 // digits of them); with more, a scan kernel turns them into prefixes first, a
-// launch more a pass.  Direct / scanned, us: 74 tiles 31.6 / 37.0, 123 tiles
-// 72.6 / 66.9, 147 tiles 53.7 / 48.1.
-static const int kSortDirectTiles = 96;
+// launch more a pass.  Whole sparse gradient, rows of 64, popular ids of a
+// million, direct / scanned, us: 48 tiles (49152 ids) 29 / 43, 74 (75392 ids)
+// 34 / 38, 74 (150000 ids) 43 / 48, 80 (81920 ids) 44 / 42, 96 (196608 ids)
+// 57 / 53, 147 (300000 ids) 75 / 70.
+static const int kSortDirectTiles = 76;
 
 template <typename T, typename Id, bool DENSE>
 static onetrans_status emb_reduce_launch(const EmbGrad& g, ReduceArgs a, cudaStream_t st) {
