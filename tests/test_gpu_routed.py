@@ -662,3 +662,30 @@ def test_weight_gradients_of_many_events_norm_wise(R, T, k, e, d):
     z, du = w * z, w * (y @ Wc["Wb2"][0].double()) * slope
     assert off(y.t() @ z.bfloat16().double(), y.t() @ z) > 2.0 ** -11
     assert off(du.bfloat16().double().t() @ x, du.t() @ x) > 2.0 ** -11
+
+
+@pytest.mark.parametrize("mode,positive", [("bf16", False), ("bf16", True), ("fp32", True)])
+def test_weight_gradients_of_millions_of_events(mode, positive):
+    """A weight gradient's float32 sums are cut into pieces of at most 8192 events.  On tensor cores a piece is 1024
+    additions (16 slots each, two terms) that truncate by 2^-23 of the partial sum at most; a term is in half of the
+    partial sums on average: within 1024 / 2 * 2^-23 = 2^-14 of the norm, and the two terms' rounding (2^-16) is of
+    either sign.  One CTA's sum over a share of all events grew with their number (here past 1e-4)."""
+    R, T, e, d = 4_000_000, 1, 16, 64
+    m, W, ev, types, wt, plan, g = inputs(mode, R, T, 1, e, d, True, "last")
+    dy = torch.randn(R, d, device="cuda", generator=g).to(DT[mode])
+    if positive:
+        wt, dy = wt.abs(), dy.abs()
+    ot.onetrans_route_events(m, types, plan)
+    grads = {f: [torch.empty(tuple(x.shape), device="cuda") for x in W[f]] for f in ("Wb1", "bb1", "Wb2", "bb2")}
+    grads["type_emb"] = torch.empty(T, d, device="cuda")
+    ot.onetrans_tokenize_routed_backward(m, ev, types, wt, plan, dy, None, None, grads, m.input_workspace(ot.OP_ROUTED_BACKWARD, R, 1))
+    assert ot.onetrans_device_status() == 0
+    ref = {f: torch.zeros(tuple(W[f][0].shape), device="cuda", dtype=torch.float64) for f in ("Wb1", "bb1", "Wb2", "bb2")}
+    for r in torch.arange(R, device="cuda").split(1 << 19):
+        x, w, y = ev[r].double(), wt[r].double(), dy[r].double()
+        _, z, slope = parts(W, 0, x)
+        du = w * (y @ W["Wb2"][0].double()) * slope
+        for f, v in (("Wb1", du.t() @ x), ("bb1", du.sum(0)), ("Wb2", (w * y).t() @ z), ("bb2", (w * y).sum(0))):
+            ref[f] += v
+    for f in ref:
+        assert float((grads[f][0].double() - ref[f]).norm() / ref[f].norm()) <= 2.0 ** -14, f

@@ -453,10 +453,16 @@ static onetrans_status tokenize_routed_impl(const onetrans_model* m, const Route
   return combine_launch<T>(a.plan, part, d, c->tokens, c->rows, st);
 }
 
-// Slices of the weight gradients: enough CTAs for the GPU's 148 SMs, no more
-// pieces than tiles.
-static int weight_slices(long long tiles, int blocks, int waves) {
-  return (int)std::max<long long>(1, std::min<long long>(tiles, cdiv(148 * waves, blocks)));
+// Slices of the weight gradients: `ctas` of them where that is no more than
+// one a tile, and as many more as keep a slice within kPieceTiles tiles.  A
+// piece is summed in float32 by one CTA, on tensor cores by additions that
+// truncate, 16 a tile: about 3e-7 of the piece is lost a tile (75392 events, 16
+// tiles a piece, 5.5e-6; 151552 events, 32 tiles, 1.0e-5).  Without the second
+// rule 10^6 events were off by 6.4e-5, 4 million by 2.5e-4, and so on; with it
+// none is by more than about 2e-5.
+static const int kPieceTiles = 64;
+static int weight_slices(long long tiles, long long ctas) {
+  return (int)std::max<long long>({1, std::min<long long>(tiles, ctas), cdiv(tiles, kPieceTiles)});
 }
 
 static onetrans_status wsum_launch(const PlanView& plan, const WeightPieces& w1, const WeightPieces& w2, int d, int e,
@@ -486,7 +492,7 @@ static onetrans_status routed_backward_simt(const onetrans_model* m, const Route
   const int nb = (int)cdiv(d, 64), eb = (int)cdiv(e, 64);
   const int n2 = nb * nb, n1 = nb * eb;
   WeightPieces w1, w2;
-  w1.slices = weight_slices(tiles, n2 + n1, 4);
+  w1.slices = weight_slices(tiles, cdiv(148 * 4, n2 + n1));   // four CTAs an SM
   w1.per = (int)cdiv(tiles, w1.slices);
   w2 = w1;
   w1.stride = (long long)d * e + d;
@@ -530,8 +536,7 @@ static onetrans_status routed_backward_tc(const onetrans_model* m, const RoutedC
   const WgCfg wc = wg_cfg(e, d);
   WgArgs w;
   std::memset(&w, 0, sizeof(w));
-  // both roles of every hidden chunk on the GPU's 148 SMs at once
-  w.p1.slices = (int)std::max<long long>(1, std::min<long long>(tiles, 74 / wc.chunks));
+  w.p1.slices = weight_slices(tiles, 74 / wc.chunks);   // both roles of every hidden chunk on the 148 SMs at once
   w.p1.per = (int)cdiv(tiles, w.p1.slices);
   w.p2 = w.p1;
   w.p1.stride = (long long)d * e + d;
