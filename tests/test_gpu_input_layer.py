@@ -166,3 +166,40 @@ def test_refusals_of_the_binding():
             ot.onetrans_tokenize_routed(m, a["ev"], a["types"], a["wt"], a["plan"], a["tok"], wsr)
     with pytest.raises(ot.OneTransError):
         ot.onetrans_route_events(m, types, plan[:256])
+
+
+def test_values_per_choice_and_gradients_of_another_shape_are_refused():
+    """A buffer of the right number of elements but another shape (the transpose's) would be read or written in the
+    wrong order: refused.  The shape itself and a flat view of it are taken."""
+    e, d, R, k = 32, 64, 6, 3
+    e, d, R, k = 32, 64, 6, 3
+    b = build(shape(n_layers=1, d=d, H=1, dff=64, L_NS=1, F=16), 5, "bf16", event_dim=e)
+    m, T = b.model, b.model.cfg.n_behaviors
+    ev, types = torch.randn(R, e, device="cuda").bfloat16(), torch.zeros(R, k, device="cuda", dtype=torch.int32)
+    plan, ws, wsb = (m.input_workspace(op, R, k) for op in (ot.OP_ROUTE, ot.OP_ROUTED, ot.OP_ROUTED_BACKWARD))
+    ot.onetrans_route_events(m, types, plan)
+    wt, tok = torch.rand(R, k, device="cuda"), torch.zeros(R, d, device="cuda", dtype=torch.bfloat16)
+
+    def grads(**other):
+        g = {"Wb1": (d, e), "bb1": (d,), "Wb2": (d, d), "bb2": (d,)}
+        out = {f: [torch.zeros(other.get(f, s), device="cuda") for _ in range(T)] for f, s in g.items()}
+        return dict(out, type_emb=torch.zeros(other.get("type_emb", (T, d)), device="cuda"))
+
+    def back(weights=wt, dw=None, **other):
+        ot.onetrans_tokenize_routed_backward(m, ev, types, weights, plan, tok, None, dw, grads(**other), wsb)
+
+    for good in (wt, wt.view(-1)):
+        ot.onetrans_tokenize_routed(m, ev, types, good, plan, tok, ws)
+        back(good, torch.empty_like(good))
+    back(Wb1=(d * e,), Wb2=(d * d,), type_emb=(T * d,))
+    for bad in (wt.view(k, R), wt.view(1, R, k), wt.view(R * k, 1)):
+        with pytest.raises(ValueError):
+            ot.onetrans_tokenize_routed(m, ev, types, bad, plan, tok, ws)
+        with pytest.raises(ValueError):
+            back(bad)
+        with pytest.raises(ValueError):
+            back(dw=torch.empty_like(bad))
+    for other in (dict(Wb1=(e, d)), dict(Wb1=(d, e, 1)), dict(bb1=(1, d)), dict(type_emb=(d, T))):
+        with pytest.raises(ValueError):
+            back(**other)
+    assert ot.onetrans_device_status() == 0

@@ -12,6 +12,7 @@ The functions carry the C names (onetrans_forward, onetrans_stage1_encode,
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Dict, Optional, Sequence
 
@@ -556,6 +557,11 @@ def _choices(types: torch.Tensor):
     return types.shape[0], types.shape[1] if types.dim() == 2 else 1
 
 
+def _per_choice(t: Optional[torch.Tensor], R: int, k: int) -> bool:
+    """None, or contiguous float32, a value per choice in their order: [R, k] or flat (not, say, [k, R])."""
+    return t is None or (tuple(t.shape) in ((R, k), (R * k,)) and t.is_contiguous() and t.dtype == torch.float32)
+
+
 def _token_rows(t: torch.Tensor, R: int, d: int, what: str):
     """(rows per sample, sample stride) of token rows [R, d] or [B, L, d] with R = B * L, the rows of a sample
     one after another (a slice x0[:, :L_S] of contiguous x0 is taken in place)."""
@@ -577,8 +583,7 @@ def _routed_args(model: Model, events, types, weights, plan, ws, *more):
     e = model.cfg.event_dim
     _need(events.dim() == 2 and tuple(events.shape) == (R, e) and events.is_contiguous() and events.dtype == model.dtype,
           "events must be a contiguous [R, event_dim] tensor of the model dtype")
-    _need(weights is None or (weights.numel() == R * k and weights.is_contiguous() and weights.dtype == torch.float32),
-          "weights must be a contiguous float32 tensor of the types' shape, or None")
+    _need(_per_choice(weights, R, k), "weights must be a contiguous float32 tensor of the types' shape, or None")
     return R, k
 
 
@@ -615,21 +620,21 @@ def onetrans_tokenize_routed_backward(model: Model, events: torch.Tensor, types:
     per, ld = _token_rows(dtokens, R, model.d, "dtokens")
     _need(devents is None or (devents.shape == events.shape and devents.is_contiguous() and devents.dtype == model.dtype),
           "devents must be a contiguous tensor like events, or None")
-    _need(dweights is None or (dweights.numel() == R * k and dweights.is_contiguous() and dweights.dtype == torch.float32),
-          "dweights must be a contiguous float32 tensor of the types' shape, or None")
+    _need(_per_choice(dweights, R, k), "dweights must be a contiguous float32 tensor of the types' shape, or None")
     T, d, e = model.cfg.n_behaviors, model.d, model.cfg.event_dim
     g = EventGrads()
     keep = []
-    for f, n in (("Wb1", d * e), ("bb1", d), ("Wb2", d * d), ("bb2", d)):
+    for f, shape in (("Wb1", (d, e)), ("bb1", (d,)), ("Wb2", (d, d)), ("bb2", (d,))):
         ts = grads[f]
-        _need(len(ts) == T and all(t.numel() == n and t.is_contiguous() and t.dtype == torch.float32 for t in ts),
+        _need(len(ts) == T and all(t.shape in (shape, (math.prod(shape),)) and t.is_contiguous() and t.dtype == torch.float32
+                                   for t in ts),
               f"grads['{f}'] must hold one contiguous float32 tensor of the weight's shape per behavior")
         _on_one_device(*ts)
         arr = (P * T)(*[t.data_ptr() for t in ts])
         keep.append(arr)
         setattr(g, f, ctypes.cast(arr, PP))
     emb = grads["type_emb"]
-    _need(emb.numel() == T * d and emb.is_contiguous() and emb.dtype == torch.float32, "grads['type_emb'] must be float32 [n_behaviors, d]")
+    _need(emb.shape in ((T, d), (T * d,)) and emb.is_contiguous() and emb.dtype == torch.float32, "grads['type_emb'] must be float32 [n_behaviors, d]")
     g.type_emb = emb.data_ptr()
     _check("onetrans_tokenize_routed_backward", lib.onetrans_tokenize_routed_backward(
         model.handle, _ptr(events), _ptr(weights), R, k, _ptr(plan), plan.numel(), _ptr(dtokens),
