@@ -107,11 +107,15 @@ ONETRANS_API onetrans_status onetrans_route_events(const onetrans_model* m, cons
  *     (r % rows_per_sample) * d elements, so that the S rows of x0
  *     [B, L_S + L_NS, d] are written in place (rows_per_sample = L_S,
  *     sample_ld = (L_S + L_NS) * d); rows_per_sample >= R: rows one after
- *     another, sample_ld is not looked at.  Elements outside those rows are left as they were.
+ *     another, sample_ld is not looked at.  Elements outside those rows are
+ *     left as they were.
  * A plan that onetrans_route_events did not make for this model's behaviours,
  * R and k sets the device status word (code 3) and nothing is written.
- * BF16 mode: the hidden row z is rounded to bf16 as the operand of the second
- * product; sums are float32, the token is rounded once. */
+ * Sums are float32, the token is rounded once.  BF16 mode with d_model a
+ * multiple of 64 up to 384, event_dim a multiple of 16 up to 128 and sample_ld
+ * a multiple of 8 runs on tensor cores: the hidden row z is rounded to bf16 as
+ * the operand of the second product, and its GELU is off by up to 2^-12 |u|
+ * more.  Other shapes keep z in float32. */
 ONETRANS_API onetrans_status onetrans_tokenize_routed(const onetrans_model* m, const void* events,
                                                       const float* weights, int64_t R, int32_t k, const void* plan,
                                                       size_t plan_bytes, void* tokens, int64_t rows_per_sample,
@@ -134,13 +138,13 @@ typedef struct {
  *   devents [R, event_dim] (mode's type) or NULL;
  *   dweights [R, k] float32 or NULL (0 where a choice is none);
  *   grads: every weight gradient (zeros for a behaviour without events).
- * BF16 mode: float32 dtokens are rounded to bf16 as matrix operands; z and
- * the pre-activation gradient enter the weight gradients' products as two
- * bf16 terms (16 bits of significand), and the event gradient's product as
- * one, rounded once more as devents are stored (two terms of either sign times
- * an infinity: an infinite dtokens or events element makes NaN of its
- * behaviour's weight gradients).  R = 0 writes the zeros of
- * grads.  The plan is checked as above. */
+ * BF16 mode: float32 dtokens are rounded to bf16 as matrix operands.  On tensor
+ * cores (the shapes above) z and the pre-activation gradient enter the weight
+ * gradients' products as two bf16 terms (16 bits of significand; an infinity in
+ * dtokens or events, which meets two terms of either sign, can make NaN where
+ * the product is infinite), and the event gradient's product as one, rounded
+ * once more as devents are stored.  Other shapes keep both in float32.  R = 0
+ * writes the zeros of grads.  The plan is checked as above. */
 ONETRANS_API onetrans_status onetrans_tokenize_routed_backward(
     const onetrans_model* m, const void* events, const float* weights, int64_t R, int32_t k, const void* plan,
     size_t plan_bytes, const void* dtokens, int32_t dtokens_mode, int64_t rows_per_sample, int64_t sample_ld,

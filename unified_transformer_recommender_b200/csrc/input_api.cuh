@@ -11,6 +11,9 @@ static bool allow_smem(K kernel, size_t bytes) {
          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
+// 148 in the rules below: the SMs of a B200, as a constant, since workspace
+// sizes are asked for without a device and the order of sums is not to depend
+// on one.
 static const long long kMaxTableRows = 0x7fffffff, kMaxGradIds = 1LL << 26;
 static const int kMaxWidth = 65536;
 

@@ -187,7 +187,7 @@ __device__ inline void load_biases(float* to, const RoutedMLP& mlp, int t, int d
 // hidden row therefore never leaves the SM.  A chunk's weights and its U
 // columns form one slot of a ring: both are free when its second product is
 // done, so the chain product - GELU - product of up to four chunks overlaps
-// (one chunk's chain takes about 2000 cycles, its products 800).  The weights
+// (one chunk's chain takes about 1600 cycles, its products 640).  The weights
 // stream through that ring from L2 (the tiles of one behaviour read the same
 // 2 d (e + d) bytes).  The gathered event rows come through cp.async into the
 // swizzled operand layout; four warps of their own take D out, weighted, as
@@ -195,10 +195,20 @@ __device__ inline void load_biases(float* to, const RoutedMLP& mlp, int t, int d
 // hidden units are computed.
 // Warps 0-7 GELU, 8-11 output, 12-15 gather, 16 weights, 17 first products,
 // 18 second products (one issuing warp would be the bottleneck).
-// 75392 events (d 256, e 64) take 24.7 us, 500 TFLOP/s: four tiles a CTA, each
-// bound by its chunks' chains (the products alone would be 9 us), the first
-// tile's gather and the last one's output uncovered.  On CUDA cores the same
-// call takes 605 us.
+// 75392 events (d 256, e 64) take 25 us, 500 TFLOP/s, four tiles a CTA (the
+// products alone would be 5.5 us).  By the roles' clocks a tile takes 8.1 K
+// cycles: for 4.9 K the output warps hold D, the one there is, while they read,
+// weight and store it; for 3.1 K the next tile's second products follow, whose
+// hidden units have been ready (0.9 K cycles of GELU a chunk).  10.7 K cycles
+// before the first D and 4 K after the last are uncovered.  On CUDA cores the
+// same call takes 605 us.
+// z is rounded to bf16 as an operand, which decides the tokens' error: relative
+// to 64 bits 2.31e-3, where the token's own rounding alone makes 1.65e-3.  GELU
+// goes by the hardware's tanh, as in the block stack: off by up to 2^-12 |u|,
+// less than z's rounding down to u of about -1.2, more in the tail (1e-3 at
+// most, where z itself is small).  A GELU that is exact there too, by an
+// exponential and a reciprocal, leaves the tokens' error at 2.31e-3 and took
+// 28.4 us against 27.2 (256 events 12.6 / 11.6).
 constexpr int kTokThreads = 608, kTokGelu = 8, kTokOut = 4;
 
 struct TokCfg {
@@ -561,19 +571,26 @@ __global__ void __launch_bounds__(256) routed_round_rows_kernel(const float* __r
 // about 2400 tensor-core cycles a step (d = 256, e = 64) each.
 // Role 1 also writes du, rounded once to bf16, as rows for the event gradient
 // and, where asked, each slot's <dz, z> over its units.
-// The bound is the compute warps' two special-function results a value (2048
-// cycles a step) with the rest of their work; their warps run apart by up to a
-// step, so what one waits for overlaps another's arithmetic.
+// The compute warps bound it.  By their clocks a step takes 5.4 K cycles, one
+// phase after the other (the warps are mostly in the same one): in role 1 2.6 K
+// for GELU and its slope (the two special-function results a value alone would
+// be 2.0 K), 0.4 K waiting for dz, 0.9 K multiplying and splitting, 0.7 K
+// storing du, 0.6 K waiting for the next U; in role 2 3.1 K for GELU and the
+// split, 1.7 K for db2, 0.7 K waiting.  The first step takes 12 K, the end of a
+// piece 4-7 K.  768 threads leave 80 registers each, and every instantiation
+// spills (d 256: 80 bytes stored and 116 loaded, with choice weights' gradients
+// 216 and 264; d 384 with them 348 and 348).
 // Warps 0-15 compute, 16-19 gather DY, 20-21 events (on their own, so that
 // the next step's do not queue behind this step's DY), 22 weights and first
 // products, 23 second products.
-// 75392 events (d 256, e 64): 72 us, 16 steps of about 4 us a CTA, of the call's
-// 108; on CUDA cores the call takes 1217 (float32).  Three event tiles in
+// 75392 events (d 256, e 64): 71 us in a list of launches, 16 steps a CTA, of
+// the call's 110; on CUDA cores the call takes 1217 (float32).  Three event tiles in
 // flight against two: 109 / 113.5 us (e <= 64; wider rows leave room for two).
 // The sums' error: the second term's rounding (2^-17 of a value) and the tensor
 // cores' float32 sums, which truncate; 5.5e-6 of dW1 over 75392 events
-// together, where float32 sums in another order differ by 3.1e-6.  One term
-// would leave 2^-9 of each value; a third costs half the products again.
+// together, where float32 sums in another order differ by 3.1e-6 (9973 events
+// of two of eight behaviours: 3.2e-6 and 1.0e-6).  One term would leave 2^-9 of
+// each value; a third costs half the products again.
 constexpr int kWgThreads = 768, kWgCompute = 16;
 
 struct WgCfg {
