@@ -415,3 +415,24 @@ def test_a_gradient_field_at_an_odd_bf16_column_is_refused():
         ot.onetrans_embedding_backward(m, row[:, 3:11], ids, torch.zeros(5, 8, device="cuda"),
                                        m.input_workspace(ot.OP_EMBEDDING_BACKWARD, 10, 8))
     assert e.value.status == ot.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("R", [4096, 4097, 37_888, 37_889, 77_824, 77_825, 81_920, 81_921, 155_648, 155_649, 327_680, 327_681])
+@pytest.mark.parametrize("V", [90, 1_000_003])
+def test_gradient_on_both_sides_of_the_size_rules(R, V):
+    """Counted and sorted ids, tiles of two and of four items a thread, each with counts added up by the passes and
+    scanned, chunks of 64, 128 and 256 positions."""
+    m, w = model("bf16"), 8
+    dout, ids = torch.randn(R, w, device="cuda").bfloat16(), make_ids("popular", R, V, R + 71)
+    ws = m.input_workspace(ot.OP_EMBEDDING_BACKWARD, R, w)
+    room = min(R, V)
+    dtable, rows = torch.full((V, w), float("nan"), device="cuda"), torch.full((room, w), 7.0, device="cuda")
+    uniq, n = torch.full((room,), -7, device="cuda", dtype=torch.int32), torch.zeros(1, device="cuda", dtype=torch.int32)
+    ot.onetrans_embedding_backward(m, dout, ids, dtable, ws)
+    ot.onetrans_embedding_backward_sparse(m, dout, ids, V, uniq, rows, n, ws)
+    s, mag, cnt = reference(dout, ids, V, 1.0)
+    check_rows(dtable, s, mag, cnt)
+    U = int(n.item())
+    assert torch.equal(uniq[:U].long(), torch.nonzero(cnt)[:, 0]) and (uniq[U:] == -7).all()
+    assert torch.equal(rows[:U], dtable[cnt > 0]) and (rows[U:] == 7.0).all()
+    assert ot.onetrans_device_status() == 0
